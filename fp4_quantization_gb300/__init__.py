@@ -22,6 +22,7 @@ NVFP4_2D = 16
 ACT_SILU = 32
 SCALE_RCEIL = 64
 SCALE_SWIZZLED = 128
+OUT_F32 = 256
 
 
 def scale_shape(R, C, flags):
@@ -35,6 +36,7 @@ OP_NVFP4 = 1
 OP_DACT = 2
 OP_ROWCOL_HOST = 3
 DEVERR_TIMEOUT = 1
+DEVERR_OFFSETS = 2
 
 STATUS_NAMES = {0: "MXQ_OK", 1: "MXQ_EINVAL", 2: "MXQ_ESHAPE", 3: "MXQ_EALIGN",
                 4: "MXQ_EARCH", 5: "MXQ_EWORKSPACE", 6: "MXQ_ECUDA"}
@@ -307,6 +309,109 @@ def nvfp4_quantize_transpose(x, flags=ROWWISE | COLWISE, *, amax=None, global_sc
         _ptr(out.get("q_row")), _ptr(out.get("s_row")), _ptr(out.get("q_t")),
         _ptr(out.get("s_t")), _ptr(workspace), ws_bytes, _ptr(dev_err), _stream(stream))
     _check(st, "nvfp4_quantize_transpose")
+    return out
+
+
+_OUT_FLAGS = {torch.bfloat16: 0, torch.float32: OUT_F32}
+
+
+def _operand(t, name, dim, dtype=torch.uint8):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dim:
+        raise TypeError(f"{name} must be a {dim}-D {dtype} tensor")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.shape
+
+
+def _product_out(out, shape, out_dtype, device):
+    """The output tensor (allocated when not given), its row stride and the
+    flags of its type."""
+    if out is None:
+        out = _empty(shape, out_dtype, device)
+    elif tuple(out.shape) != shape or not out.is_cuda:
+        raise ValueError(f"out must be a CUDA tensor of shape {shape}")
+    if out.dtype not in _OUT_FLAGS:
+        raise TypeError("the output type is torch.bfloat16 or torch.float32")
+    if shape[-1] > 1 and out.stride(-1) != 1:
+        raise ValueError("out needs a unit column stride")
+    ldo = out.stride(-2) if shape[-2] > 1 else max(shape[-1], 1)
+    return out, ldo, _OUT_FLAGS[out.dtype]
+
+
+def mx_grouped_gemm(x_q, x_s, w_q, w_s, offsets, *, out=None, out_dtype=torch.bfloat16,
+                    dev_err=None, stream=None):
+    """Rows sorted by expert times their experts' weights: x_q [M,K] / x_s
+    [M,K/32] and w_q [E,N,K] / w_s [E,N,K/32] as mx_quantize_rowcol writes
+    them (ROWWISE, row-major scales), offsets [E+1] int32; returns [M,N]
+    bf16 or fp32.  Rows in no group are not written.  For the input gradient
+    pass the gradient's rows and the weights' COLWISE codes [E,K,N]."""
+    M, K = _operand(x_q, "x_q", 2)
+    E, N, Kw = _operand(w_q, "w_q", 3)
+    if Kw != K or tuple(_operand(x_s, "x_s", 2)) != (M, K // 32) \
+            or tuple(_operand(w_s, "w_s", 3)) != (E, N, K // 32):
+        raise ValueError("x_q [M,K], x_s [M,K/32], w_q [E,N,K] and w_s [E,N,K/32] do not agree")
+    if tuple(_operand(offsets, "offsets", 1, torch.int32)) != (E + 1,):
+        raise ValueError("offsets must have one entry more than there are experts")
+    out, ldo, flags = _product_out(out, (M, N), out_dtype, x_q.device)
+    st = _lib.lib().mx_grouped_gemm(
+        x_q.data_ptr(), x_s.data_ptr(), w_q.data_ptr(), w_s.data_ptr(), offsets.data_ptr(), M, N,
+        K, E, flags, out.data_ptr(), ldo, _ptr(dev_err), _stream(stream))
+    _check(st, "mx_grouped_gemm")
+    return out
+
+
+def mx_grouped_wgrad(g_q, g_s, x_q, x_s, offsets, *, out=None, out_dtype=torch.float32,
+                     dev_err=None, stream=None):
+    """The weights' gradients of mx_grouped_gemm: g_q [N,M] / g_s [N,M/32]
+    and x_q [K,M] / x_s [K,M/32] as mx_quantize_rowcol writes them
+    (COLWISE), offsets [E+1] int32, multiples of 32; returns [E,N,K] fp32 or
+    bf16."""
+    N, M = _operand(g_q, "g_q", 2)
+    K, Mx = _operand(x_q, "x_q", 2)
+    if Mx != M or tuple(_operand(g_s, "g_s", 2)) != (N, M // 32) \
+            or tuple(_operand(x_s, "x_s", 2)) != (K, M // 32):
+        raise ValueError("g_q [N,M], g_s [N,M/32], x_q [K,M] and x_s [K,M/32] do not agree")
+    E = _operand(offsets, "offsets", 1, torch.int32)[0] - 1
+    if E < 0:
+        raise ValueError("offsets must have one entry more than there are experts")
+    out, _, flags = _product_out(out, (E, N, K), out_dtype, g_q.device)
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    st = _lib.lib().mx_grouped_wgrad(
+        g_q.data_ptr(), g_s.data_ptr(), x_q.data_ptr(), x_s.data_ptr(), offsets.data_ptr(), M, N,
+        K, E, flags, out.data_ptr(), _ptr(dev_err), _stream(stream))
+    _check(st, "mx_grouped_wgrad")
+    return out
+
+
+def nvfp4_gemv(x, w_q, w_s, global_scale, *, experts=None, share=1, out=None,
+               out_dtype=torch.bfloat16, stream=None):
+    """Few rows times NVFP4 weights as nvfp4_quantize_transpose writes them
+    (ROWWISE): x [T,K] bf16 with w_q [N,K/2] / w_s [N,K/16] / global_scale
+    [1], or with experts [T*share] int32 and w_q [E,N,K/2] / w_s [E,N,K/16] /
+    global_scale [E], where `share` output rows in turn read one row of x
+    and a row whose expert is not in [0, E) is zero.  Returns [T*share,N]
+    bf16 or fp32."""
+    ldx = _input(x)
+    T, K = x.shape
+    dim = 2 if experts is None else 3
+    N = _operand(w_q, "w_q", dim)[-2]
+    E = 1 if experts is None else w_q.shape[0]
+    lead = () if experts is None else (E,)
+    if K % 2 or tuple(w_q.shape) != lead + (N, K // 2) \
+            or tuple(_operand(w_s, "w_s", dim)) != lead + (N, K // 16):
+        raise ValueError("x [T,K], w_q [(E,) N,K/2] and w_s [(E,) N,K/16] do not agree")
+    if _operand(global_scale, "global_scale", 1, torch.float32)[0] != E:
+        raise ValueError("global_scale must have one entry for each expert")
+    if experts is not None and tuple(_operand(experts, "experts", 1, torch.int32)) != (T * share,):
+        raise ValueError("experts must have T * share entries")
+    out, ldo, flags = _product_out(out, (T * share, N), out_dtype, x.device)
+    st = _lib.lib().nvfp4_gemv(
+        x.data_ptr(), ldx, w_q.data_ptr(), w_s.data_ptr(), global_scale.data_ptr(),
+        _ptr(experts), T, share, N, K, E, flags, out.data_ptr(), ldo, _stream(stream))
+    _check(st, "nvfp4_gemv")
     return out
 
 

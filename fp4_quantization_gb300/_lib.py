@@ -35,6 +35,12 @@ SIGNATURES = {
     "bf16_amax": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp]),
     "nvfp4_quantize_transpose": (ctypes.c_int, [_vp, _i64, _i64, _i64, _u32, _vp, _vp, _vp, _vp,
                                                 _vp, _vp, _vp, _sz, _vp, _vp]),
+    "mx_grouped_gemm": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _u32, _vp,
+                                       _i64, _vp, _vp]),
+    "mx_grouped_wgrad": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _u32,
+                                        _vp, _vp, _vp]),
+    "nvfp4_gemv": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64,
+                                  _u32, _vp, _i64, _vp]),
     "mxq_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_uint64, _vp, _vp]),
 }
 

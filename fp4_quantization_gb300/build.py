@@ -26,6 +26,9 @@ UNITS = [
     ("nvfp4_kernels.cu", [], "nvfp4_kernels.o"),
     ("mxq_noalloc.cu", [], "mxq_noalloc.o"),
     ("mxq_host.cu", [], "mxq_host.o"),
+    ("mxq_products.cu", [], "mxq_products.o"),
+    ("mx_product_kernels.cu", [], "mx_product_kernels.o"),
+    ("nvfp4_gemv_kernels.cu", [], "nvfp4_gemv_kernels.o"),
 ]
 SOURCES = sorted({src for src, _, _ in UNITS})
 

@@ -10,6 +10,7 @@
 
 #include "mxq.h"
 #include "mxq_internal.h"
+#include "mxq_products.h"
 
 namespace {
 
@@ -23,6 +24,25 @@ struct DeviceInfo {
 };
 DeviceInfo g_devices[kMaxDevices];
 std::mutex g_device_mutex;
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+bool load_encoder() {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  return g_encode != nullptr;
+}
+
+}  // namespace
+
+namespace mxq {
 
 // Looks up (once per device) whether the current device is sm_103 and how
 // many SMs it has.
@@ -46,27 +66,12 @@ mxq_status current_device(int* num_sms) {
   return MXQ_OK;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-bool load_encoder() {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  return g_encode != nullptr;
-}
-
 // Encodes a tensor map of `rank` dimensions (innermost first) with no
 // swizzle; out-of-range loads read 0 and out-of-range stores are dropped.
 mxq_status encode_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
                       const cuuint64_t* dims, const cuuint64_t* strides_bytes,
                       const cuuint32_t* box,
-                      CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE) {
+                      CUtensorMapSwizzle swizzle) {
   if (!load_encoder()) return MXQ_ECUDA;
   const cuuint32_t elem_strides[5] = {1, 1, 1, 1, 1};
   const CUresult r = g_encode(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base),
@@ -76,6 +81,13 @@ mxq_status encode_map(CUtensorMap* map, CUtensorMapDataType type, int rank, cons
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MXQ_OK : MXQ_ECUDA;
 }
+
+}  // namespace mxq
+
+namespace {
+
+using mxq::current_device;
+using mxq::encode_map;
 
 // 2-D bf16 map over x[rows][cols] (row stride ldx elements).
 mxq_status encode_bf16_map(CUtensorMap* map, const void* x, int64_t rows, int64_t cols,

@@ -1,0 +1,75 @@
+// mxq_products.h -- launch arguments and launchers of the products on
+// block-scaled operands, and the host helpers of mxq_api.cu that their entry
+// points share.  Not installed.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "mxq.h"
+
+namespace mxq {
+
+constexpr int GROUPS_MAX = 1024;      // experts of one grouped call
+constexpr uint64_t PRODUCT_TIMEOUT_NS = 1000000000ull;   // 1 s per wait
+
+// One grouped product: tiles of out = A B^T, where A's and B's rows are codes
+// along the contraction axis.  Forward: A is [limit][depth], B is
+// [groups][b_rows][depth], and group g owns A's (and out's) rows
+// [offsets[g], offsets[g + 1]).  Weight gradient (wgrad != 0): A is
+// [a_rows][limit], B is [b_rows][limit], and group g owns the contraction
+// range [offsets[g], offsets[g + 1]) and the output matrix g.
+struct GroupedArgs {
+  const int32_t* offsets;   // [groups + 1], device
+  int groups;
+  int limit;                // M: no offset is above it
+  int a_rows;               // wgrad: N
+  int b_rows;               // forward: N; wgrad: K
+  int depth;                // forward: K
+  const uint8_t* a_s;       // E8M0 scales, s_ld bytes a row
+  const uint8_t* b_s;
+  int64_t s_ld;
+  void* out;
+  int64_t ldo;              // elements between output rows
+  int out_f32;              // 1: fp32, 0: bf16
+  int out_vec;              // output rows start on 16-byte boundaries
+  uint32_t* dev_err;
+  uint64_t timeout_ns;
+};
+
+struct GroupedMaps {
+  CUtensorMap a;            // 2-D codes, box 128 bytes x 128 rows, 128-byte swizzle
+  CUtensorMap b;            // 3-D codes (depth, row, group), box 128 bytes x tile columns x 1
+};
+
+// Columns of one output tile (B rows of one copy) for a call of this size.
+int grouped_tile_cols(int64_t rows, int64_t cols, int groups, int num_sms);
+cudaError_t launch_grouped(const GroupedMaps& maps, const GroupedArgs& a, bool wgrad,
+                           int tile_cols, int num_sms, cudaStream_t stream);
+
+struct GemvArgs {
+  const uint16_t* x;        // bf16 [rows / share][ldx]
+  int64_t ldx;
+  int rows, n, k;
+  const uint8_t* w_q;       // [experts][n][k / 2]
+  const uint8_t* w_s;       // [experts][n][k / 16]
+  const float* w_global;    // [experts]
+  const int32_t* experts;   // [rows] or null
+  int num_experts;
+  int share;
+  void* out;
+  int64_t ldo;
+  int out_f32;
+};
+
+cudaError_t launch_nvfp4_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream);
+
+// Host helpers (mxq_api.cu).
+mxq_status current_device(int* num_sms);
+mxq_status encode_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
+                      const cuuint64_t* dims, const cuuint64_t* strides_bytes,
+                      const cuuint32_t* box,
+                      CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE);
+
+}  // namespace mxq

@@ -5,7 +5,9 @@
  * scale per 32-element block) rowwise and colwise from a single HBM read,
  * optionally fused with a dbias column sum, a tanh-GELU or a SwiGLU gate, and
  * into NVFP4 (E2M1 codes, one E4M3 scale per 16 elements, one fp32 tensor
- * scale) rowwise and transposed.
+ * scale) rowwise and transposed; and it multiplies what it quantized: MXFP8
+ * products grouped by expert, their weight gradients, and NVFP4 weights times
+ * a few rows.
  *
  * Kernel families this covers (TransformerEngine PR #3291 "Fix pointer
  * arithmatic to generate correct LDS/STS instructions", results tables
@@ -79,11 +81,15 @@ enum {
     MXQ_ACT_SILU = 32,      /* silu: SwiGLU gate (the default of the gated */
                             /* calls), its derivative (mx_quantize_dact)   */
     MXQ_SCALE_RCEIL = 64,   /* MXFP8 calls: ceil-style E8M0 rule, below    */
-    MXQ_SCALE_SWIZZLED = 128 /* MXFP8 calls: scales in 128x4 tiles, below   */
+    MXQ_SCALE_SWIZZLED = 128,/* MXFP8 calls: scales in 128x4 tiles, below   */
+    MXQ_OUT_F32 = 256       /* products: fp32 output instead of bf16       */
 };
 
 /* bits of *dev_err */
-enum { MXQ_DEVERR_TIMEOUT = 1 };
+enum {
+    MXQ_DEVERR_TIMEOUT = 1,
+    MXQ_DEVERR_OFFSETS = 2  /* grouped products: bad group offsets, below  */
+};
 
 /* operation ids for mxq_workspace_bytes */
 enum { MXQ_OP_ROWCOL = 0, MXQ_OP_NVFP4 = 1, MXQ_OP_DACT = 2, MXQ_OP_ROWCOL_HOST = 3 };
@@ -312,6 +318,79 @@ MXQ_API mxq_status nvfp4_quantize_transpose(const void* x, int64_t M, int64_t K,
                                     uint8_t* q_row, uint8_t* s_row, uint8_t* q_t, uint8_t* s_t,
                                     void* workspace, size_t workspace_bytes, uint32_t* dev_err,
                                     mxq_stream_t stream);
+
+/*
+ * mx_grouped_gemm -- rows sorted by expert times their experts' weights.
+ *
+ * Operation: for every group e < E and row offsets[e] <= m < offsets[e + 1],
+ * out[m][n] = sum_k X[m][k] * W[e][n][k], with X[m][k] = E4M3(x_q[m][k]) *
+ * 2^(x_s[m][k / 32] - 127) and W alike: the operands mx_quantize_rowcol
+ * writes with MXQ_ROWWISE (row-major scales), products exact, sums in fp32,
+ * one rounding to bf16 (none with MXQ_OUT_F32).  The input gradient dX = dY W
+ * is the same call: dY rowwise as x, and as w each expert's weight [N][K]
+ * quantized MXQ_COLWISE (its q_col [K][N], s_col [K][N/32]).  E = 1 with
+ * offsets {0, M} is a plain product.
+ *
+ *   x_q [M][K], x_s [M][K/32]; w_q [E][N][K], w_s [E][N][K/32]; K % 32 == 0;
+ *           M and N are any.  A scale code of 255 is NaN.
+ *   offsets [E + 1] int32 on the device, not decreasing, within [0, M]; a
+ *           group may be empty, and rows in no group are not written.
+ *           Offsets that break this set MXQ_DEVERR_OFFSETS in *dev_err and
+ *           nothing is written.  E <= 1024.
+ *   out     [M][ldo] bf16 or fp32, aligned to its element (16-byte aligned
+ *           rows are written with wider stores); ldo >= N.
+ *   K == 0 writes zeros; M, N or E == 0 is a valid empty call.
+ * The inputs are 16-byte aligned.  Results do not depend on how the rows
+ * fall into tiles: an element is always summed in the order of k.
+ */
+MXQ_API mxq_status mx_grouped_gemm(const uint8_t* x_q, const uint8_t* x_s, const uint8_t* w_q,
+                                   const uint8_t* w_s, const int32_t* offsets, int64_t M,
+                                   int64_t N, int64_t K, int64_t E, uint32_t flags, void* out,
+                                   int64_t ldo, uint32_t* dev_err, mxq_stream_t stream);
+
+/*
+ * mx_grouped_wgrad -- the weights' gradients of mx_grouped_gemm.
+ *
+ * Operation: dw[e][n][k] = sum over offsets[e] <= m < offsets[e + 1] of
+ * G[m][n] * X[m][k], with G and X quantized along m: the operands that
+ * mx_quantize_rowcol writes with MXQ_COLWISE for dY [M][N] and x [M][K].
+ * Sums in fp32; dw bf16, or fp32 with MXQ_OUT_F32.
+ *
+ *   g_q [N][M], g_s [N][M/32]; x_q [K][M], x_s [K][M/32]; M % 32 == 0; N and
+ *           K are any.
+ *   offsets as for mx_grouped_gemm, and multiples of 32 (a block of 32 rows
+ *           has one scale, so no group may start or end inside one: pad
+ *           groups with zero rows).
+ *   dw      [E][N][K], every element written (zeros for an empty group).
+ */
+MXQ_API mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, const uint8_t* x_q,
+                                    const uint8_t* x_s, const int32_t* offsets, int64_t M,
+                                    int64_t N, int64_t K, int64_t E, uint32_t flags, void* dw,
+                                    uint32_t* dev_err, mxq_stream_t stream);
+
+/*
+ * nvfp4_gemv -- few rows of bf16 times NVFP4 weights.
+ *
+ * Operation: out[r][n] = G[e] * sum_k x[r / share][k] * E4M3(w_s[e][n][k/16])
+ * * E2M1(w_q[e][n][k]) for r < T * share, with e = experts[r], or 0 when
+ * experts is NULL: the operands that nvfp4_quantize_transpose writes with
+ * MXQ_ROWWISE for each expert's weight [N][K].  Sums in fp32; out bf16, or
+ * fp32 with MXQ_OUT_F32.
+ *
+ *   x       [T][ldx] bf16, ldx % 8 == 0; K % 32 == 0; N is any.
+ *   share   output rows that read one row of x (a token's experts), >= 1.
+ *   w_q [E][N][K/2], w_s [E][N][K/16], w_global [E] fp32 on the device.
+ *   experts [T * share] int32 on the device: a row whose expert is negative
+ *           or >= E is zero (it belongs to another rank, or to no token).
+ *           NULL: one weight (E == 1, share == 1).
+ *   out     [T * share][ldo].
+ * Meant for up to 16 rows of each expert; more are right, and read the
+ * weights once for every 16.
+ */
+MXQ_API mxq_status nvfp4_gemv(const void* x, int64_t ldx, const uint8_t* w_q, const uint8_t* w_s,
+                              const float* w_global, const int32_t* experts, int64_t T,
+                              int64_t share, int64_t N, int64_t K, int64_t E, uint32_t flags,
+                              void* out, int64_t ldo, mxq_stream_t stream);
 
 /*
  * mxq_selftest_bounded_wait -- launches one warp that waits on a barrier
