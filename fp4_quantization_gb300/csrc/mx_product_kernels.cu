@@ -76,16 +76,39 @@ struct Walk {
   }
 };
 
-// 16 scale bytes at byte `at` of a row-major scale matrix, `valid` of them
-// inside the row (the others read 0).
-__device__ __forceinline__ uint4 load_scales(const uint8_t* p, int valid) {
-  if (valid >= 16 && (reinterpret_cast<uintptr_t>(p) & 15) == 0)
-    return __ldg(reinterpret_cast<const uint4*>(p));
-  uint32_t w[4] = {0, 0, 0, 0};
+// 16 scale bytes from p on, of a row with `valid` bytes left, in a matrix that
+// ends at `end`.  Rows of scales start at any byte, so the bytes come from the
+// one or two 16-byte blocks around them; what follows the row's bytes is read
+// by no instruction.  Blocks that the matrix's end cuts are read by bytes.
+__device__ __forceinline__ uint4 load_scales(const uint8_t* p, int valid, const uint8_t* end) {
+  if (valid <= 0) return make_uint4(0, 0, 0, 0);
+  const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15;
+  const uint8_t* block = p - shift;
+  const bool two = shift + min(valid, 16) > 16;
+  if (block + (two ? 32 : 16) > end) {
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (i < valid) w[i / 4] |= static_cast<uint32_t>(__ldg(p + i)) << (8 * (i % 4));
-  return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 16; ++i)
+      if (i < valid) w[i / 4] |= static_cast<uint32_t>(__ldg(p + i)) << (8 * (i % 4));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  const uint4 lo = __ldg(reinterpret_cast<const uint4*>(block));
+  if (shift == 0) return lo;
+  const uint4 hi = two ? __ldg(reinterpret_cast<const uint4*>(block) + 1) : lo;
+  uint32_t w[7] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z};
+  if (shift & 8) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 2];
+    w[5] = hi.w;
+  }
+  if (shift & 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = w[i + 1];
+    w[4] = w[5];
+  }
+  const uint32_t bits = 8 * (shift & 3);
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
 }
 
 // Writes row r's scales of the four stages of a chunk into their tiles.
@@ -305,6 +328,8 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
   } else if (warp >= 4) {
     // ---- scales: thread r takes rows r of A and r, r + 128 of B ----
     const int r = tid - 128;
+    const uint8_t* a_end = a.a_s + static_cast<int64_t>(WGRAD ? a.a_rows : a.limit) * a.s_ld;
+    const uint8_t* b_end = a.b_s + (WGRAD ? 1 : a.groups) * static_cast<int64_t>(a.b_rows) * a.s_ld;
     uint32_t chunk = 0;
     while (ok && walk.template next<BN>(a, tile)) {
       const int steps = (tile.depth + STEP_K - 1) / STEP_K;
@@ -318,12 +343,13 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
       for (int k = 0; k < steps; k += CHUNK, ++chunk) {
         const uint32_t c = chunk % S::SCALE_CHUNKS;
         const int at = k * (STEP_K / 32), valid = blocks - at;
-        const uint4 va = load_scales(ap + at, ahas ? valid : 0);
+        const uint4 va = load_scales(ap + at, ahas ? valid : 0, a_end);
         uint4 vb[S::B_TILES];
 #pragma unroll
         for (int b = 0; b < S::B_TILES; ++b)
           vb[b] = load_scales(bp + b * 128 * a.s_ld + at,
-                              tile.n0 + r + b * 128 < a.b_rows && r + b * 128 < BN ? valid : 0);
+                              tile.n0 + r + b * 128 < a.b_rows && r + b * 128 < BN ? valid : 0,
+                              b_end);
         if (chunk >= S::SCALE_CHUNKS &&
             !mbar_wait_bounded(sc_empty + 8 * c, (chunk / S::SCALE_CHUNKS - 1) & 1, a.timeout_ns)) {
           ok = false;
