@@ -12,66 +12,80 @@
 namespace mxq {
 namespace {
 
-constexpr int TILE_M = 128;           // output rows of a tile: the instruction's M
+constexpr int ROWS = 128;             // output rows of a CTA's tile
 constexpr int STEP_K = 128;           // contraction bytes of one pipeline stage: a swizzle row
 constexpr int CHUNK = 4;              // stages that share one set of scale tiles (16 bytes a row)
+constexpr int AHEAD = 2;              // chunks whose scales are on their way into registers
 constexpr int THREADS = 320;          // 4 epilogue, 4 scale, 1 copy, 1 issuing warp
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t SCALE_COL = 480;   // first tensor-memory column of the scales
+// Contraction values after which an fp32 output's sum is taken out of tensor
+// memory and added in fp32: the tensor cores cut their sums off instead of
+// rounding them, which is 1.3e-6 of the result after 14336 values and 2.7e-7
+// after this many.
+constexpr int SEGMENT = 4096;
 
-template <int BN>
+// A tile of ROWS * CTAS rows and BN columns, worked on by one CTA or a pair.
+template <int CTAS, int BN>
 struct Shape {
-  static constexpr int A_BYTES = TILE_M * STEP_K;
-  static constexpr int B_BYTES = BN * STEP_K;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN == 256 ? 4 : 5;
+  static constexpr int A_BYTES = ROWS * STEP_K;
+  static constexpr int B_ROWS = BN / CTAS;                          // of each CTA
+  static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * STEP_K;
+  static constexpr int STAGES = STAGE_BYTES > 40 * 1024 ? 4 : 5;
   static constexpr int B_TILES = (BN + 127) / 128;                  // scale tiles of B a stage
   static constexpr int SCALE_BYTES = CHUNK * 512 * (1 + B_TILES);   // one scale chunk
   static constexpr int SCALE_CHUNKS = 2;
+  static constexpr int OUT_BYTES = 4 * 32 * 128;                    // a 32-row x 128-byte patch a warp
   // Column of accumulator s.  Two 256-column accumulators share 32 columns.
   static constexpr uint32_t acc_col(uint32_t s) { return s * (BN == 256 ? 224 : BN); }
   static constexpr int TABLE_BYTES = 2 * (GROUPS_MAX + 1) * 4;
   static constexpr int BARRIERS = 2 * STAGES + 2 * SCALE_CHUNKS + 4 + 1;
   static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + SCALE_CHUNKS * SCALE_BYTES +
-                              TABLE_BYTES + BARRIERS * 8 + 64;
+                              OUT_BYTES + TABLE_BYTES + BARRIERS * 8 + 16;
 };
 
 // Where a tile lies: its group, its first row and column in the group's
-// output, and the group's rows and contraction range.
+// output, and the group's rows and the tile's contraction range.
 struct Tile {
   int g, m0, n0;
   int rows;         // rows of the group's output
-  int first, depth; // contraction range (wgrad: first row of the group; forward: 0)
+  int first, depth; // contraction range
+  bool add;         // to what an earlier range of the same tile has written
 };
 
-// Walks the tiles of this CTA in order.  Inside a group the row tiles of a
-// band of 16 run fastest, so a wave's tiles share their rows and read each
-// column tile's codes from memory once a band.
-template <bool WGRAD>
+// Walks the tiles of this CTA (or pair) in order.  Inside a group the row
+// tiles of a band of 2048 rows run fastest, so a wave's tiles share their rows
+// and each column tile's codes come from memory once a band.
+template <int CTAS, int BN, bool WGRAD>
 struct Walk {
   const int* off;
   const int* start;     // first tile of each group, and the total
   int groups, tiles_n;
-  int t, g;
+  int t, g, done;       // done: contraction values of tile t that are behind
 
-  template <int BN>
   __device__ __forceinline__ bool next(const GroupedArgs& a, Tile& tile) {
     if (t >= start[groups]) return false;
     while (t >= start[g + 1]) ++g;
     const int lo = off[g], rows_g = off[g + 1] - lo;
+    const int whole = WGRAD ? rows_g : a.depth;
     tile.g = g;
     tile.rows = WGRAD ? a.a_rows : rows_g;
-    tile.first = WGRAD ? lo : 0;
-    tile.depth = WGRAD ? rows_g : a.depth;
-    constexpr int BAND = 16;
-    const int tiles_m = (tile.rows + TILE_M - 1) / TILE_M;
+    tile.first = (WGRAD ? lo : 0) + done;
+    tile.depth = a.out_f32 ? min(whole - done, SEGMENT) : whole;
+    tile.add = done > 0;
+    constexpr int BAND = 2048 / (ROWS * CTAS);
+    const int tiles_m = (tile.rows + ROWS * CTAS - 1) / (ROWS * CTAS);
     int i = t - start[g];
     const int band = i / (BAND * tiles_n);
     i -= band * BAND * tiles_n;
     const int height = min(BAND, tiles_m - band * BAND);
-    tile.m0 = (band * BAND + i % height) * TILE_M;
+    tile.m0 = (band * BAND + i % height) * (ROWS * CTAS);
     tile.n0 = i / height * BN;
-    t += gridDim.x;
+    done += tile.depth;
+    if (done == whole) {
+      done = 0;
+      t += gridDim.x / CTAS;
+    }
     return true;
   }
 };
@@ -126,50 +140,71 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return d;
 }
 
-// One lane's 32 consecutive columns of an output row; `cols` of them exist.
-__device__ __forceinline__ void store_row(const GroupedArgs& a, int64_t row, int col, int cols,
-                                          const uint32_t (&v)[32]) {
-  if (a.out_f32) {
-    float* p = static_cast<float*>(a.out) + row * a.ldo + col;
+// Writes a warp's patch of 32 rows x 128 bytes (64 bf16 or 32 fp32 columns),
+// staged in shared memory with 16-byte units swizzled by row, to `rows` rows of
+// the output at `col`; `cols` columns exist.  Whole patches of 16-byte aligned
+// rows leave as full 128-byte lines (four rows an instruction), others by
+// elements, a row at a time.
+__device__ __forceinline__ void store_patch(const GroupedArgs& a, uint32_t patch, int lane,
+                                            int64_t row, int rows, int col, int cols, bool add) {
+  const int width = a.out_f32 ? 32 : 64;
+  if (a.out_vec && cols >= width) {
+    const int u = lane % 8;
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      if (a.out_vec && i + 4 <= cols) {
-        stg128(p + i, v[i], v[i + 1], v[i + 2], v[i + 3]);
-      } else {
-#pragma unroll
-        for (int j = i; j < i + 4; ++j)
-          if (j < cols) p[j] = __uint_as_float(v[j]);
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + lane / 8;
+      uint4 v = lds128(patch + r * 128 + ((u ^ (r & 7)) << 4));
+      if (r < rows) {
+        if (a.out_f32) {
+          float* p = static_cast<float*>(a.out) + (row + r) * a.ldo + col + 4 * u;
+          if (add) {
+            const float4 o = *reinterpret_cast<const float4*>(p);
+            v = make_uint4(__float_as_uint(__uint_as_float(v.x) + o.x),
+                           __float_as_uint(__uint_as_float(v.y) + o.y),
+                           __float_as_uint(__uint_as_float(v.z) + o.z),
+                           __float_as_uint(__uint_as_float(v.w) + o.w));
+          }
+          stg128(p, v.x, v.y, v.z, v.w);
+        } else {
+          stg128(static_cast<uint16_t*>(a.out) + (row + r) * a.ldo + col + 8 * u, v.x, v.y, v.z,
+                 v.w);
+        }
       }
     }
-  } else {
-    uint16_t* p = static_cast<uint16_t*>(a.out) + row * a.ldo + col;
+    return;
+  }
+  for (int r = 0; r < rows; ++r) {
+    const uint32_t line = patch + r * 128;
+    if (a.out_f32) {
+      if (lane < cols) {
+        float v = __uint_as_float(lds32(line + (((lane / 4) ^ (r & 7)) << 4) + lane % 4 * 4));
+        float* p = static_cast<float*>(a.out) + (row + r) * a.ldo + col + lane;
+        *p = add ? v + *p : v;
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = pack_bf16(__uint_as_float(v[i + 2 * j]), __uint_as_float(v[i + 2 * j + 1]));
-      if (a.out_vec && i + 8 <= cols) {
-        stg128(p + i, w[0], w[1], w[2], w[3]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (i + j < cols) p[i + j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j % 2)));
+      for (int h = 0; h < 2; ++h) {
+        const int c = lane + 32 * h;
+        const uint32_t v = lds32(line + (((c / 8) ^ (r & 7)) << 4) + c % 8 / 2 * 4);
+        if (c < cols)
+          static_cast<uint16_t*>(a.out)[(row + r) * a.ldo + col + c] =
+              static_cast<uint16_t>(v >> (16 * (c % 2)));
       }
     }
   }
 }
 
-template <int BN, bool WGRAD>
+template <int CTAS, int BN, bool WGRAD>
 __global__ void __launch_bounds__(THREADS, 1)
 mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a) {
-  using S = Shape<BN>;
+  using S = Shape<CTAS, BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_up_shared<1024>(smem_raw);
   const uint32_t stages = smem_addr(smem);
   const uint32_t scales = stages + S::STAGES * S::STAGE_BYTES;
+  const uint32_t patches = scales + S::SCALE_CHUNKS * S::SCALE_BYTES;
   int* off = reinterpret_cast<int*>(smem + S::STAGES * S::STAGE_BYTES +
-                                    S::SCALE_CHUNKS * S::SCALE_BYTES);
+                                    S::SCALE_CHUNKS * S::SCALE_BYTES + S::OUT_BYTES);
   int* start = off + GROUPS_MAX + 1;
   const uint32_t bars = smem_addr(start + GROUPS_MAX + 1);   // 8-byte aligned: 2 (MAX + 1) words
   const uint32_t full = bars, empty = full + 8 * S::STAGES;
@@ -180,27 +215,31 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int tiles_n = (a.b_rows + BN - 1) / BN;
+  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;   // 0: the CTA that issues
 
+  // full, sc_full and acc_empty are waited on by the issuing CTA alone, and
+  // with pairs the other CTA's copies and warps arrive there; the others are
+  // each CTA's own.
   if (tid == 0) {
     for (int i = 0; i < S::STAGES; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < S::SCALE_CHUNKS; ++i) {
-      mbar_init(sc_full + 8 * i, 128);
+      mbar_init(sc_full + 8 * i, 4 * CTAS);
       mbar_init(sc_empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + 8 * i, 1);
-      mbar_init(acc_empty + 8 * i, 128);
+      mbar_init(acc_empty + 8 * i, 4 * CTAS);
     }
     mbar_init(drain, 1);
     fence_barrier_init();
   }
-  if (warp == 9) tmem_alloc(smem_addr(tmem_slot), TMEM_COLS);
+  if (warp == 9) tmem_alloc<CTAS>(smem_addr(tmem_slot), TMEM_COLS);
 
-  // Offsets, checked, and the groups' first tiles (each warp's share scanned
-  // by shuffles, 32 groups a step).
+  // Offsets, checked, and the groups' first tiles (scanned by one warp, 32
+  // groups a step).
   bool bad = false;
   for (int i = tid; i <= a.groups; i += THREADS) {
     const int v = a.offsets[i];
@@ -215,7 +254,7 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
       int n = 0;
       if (!bad && i + lane < a.groups) {
         const int rows = WGRAD ? a.a_rows : off[i + lane + 1] - off[i + lane];
-        n = (rows + TILE_M - 1) / TILE_M * tiles_n;
+        n = (rows + ROWS * CTAS - 1) / (ROWS * CTAS) * tiles_n;
       }
       int sum = n;
 #pragma unroll
@@ -230,21 +269,23 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
     if (bad && lane == 0 && blockIdx.x == 0 && a.dev_err) atomicOr(a.dev_err, MXQ_DEVERR_OFFSETS);
   }
   tc_fence_before_sync();
+  if constexpr (CTAS == 2) cluster_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
-  Walk<WGRAD> walk{off, start, a.groups, tiles_n, static_cast<int>(blockIdx.x), 0};
+  Walk<CTAS, BN, WGRAD> walk{off, start, a.groups, tiles_n, static_cast<int>(blockIdx.x) / CTAS, 0, 0};
   Tile tile;
   bool ok = true;
 
   if (warp == 8) {
-    // ---- copies: one stage of A and B codes at a time ----
+    // ---- copies: a stage of this CTA's rows of A and of B at a time ----
     if (lane == 0) {
       uint32_t it = 0;
-      while (ok && walk.template next<BN>(a, tile)) {
+      while (ok && walk.next(a, tile)) {
         const int steps = (tile.depth + STEP_K - 1) / STEP_K;
-        const int ay = WGRAD ? tile.m0 : off[tile.g] + tile.m0;
+        const int ay = (WGRAD ? 0 : off[tile.g]) + tile.m0 + static_cast<int>(rank) * ROWS;
+        const int by = tile.n0 + static_cast<int>(rank) * S::B_ROWS;
         const int bz = WGRAD ? 0 : tile.g;
         for (int k = 0; k < steps; ++k, ++it) {
           const uint32_t s = it % S::STAGES;
@@ -254,31 +295,38 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
             break;
           }
           const uint32_t dst = stages + s * S::STAGE_BYTES, bar = full + 8 * s;
-          mbar_arrive_expect_tx(bar, S::STAGE_BYTES);
+          if (rank == 0) mbar_arrive_expect_tx(bar, CTAS * S::STAGE_BYTES);
           const int x = tile.first + k * STEP_K;
-          tma_load_2d(dst, &maps.a, x, ay, bar);
-          tma_load_3d(dst + S::A_BYTES, &maps.b, x, tile.n0, bz, bar);
+          if constexpr (CTAS == 2) {
+            const uint32_t there = cluster_addr(bar, 0);
+            tma_load_2d_pair(dst, &maps.a, x, ay, there);
+            tma_load_3d_pair(dst + S::A_BYTES, &maps.b, x, by, bz, there);
+          } else {
+            tma_load_2d(dst, &maps.a, x, ay, bar);
+            tma_load_3d(dst + S::A_BYTES, &maps.b, x, by, bz, bar);
+          }
         }
       }
-      // After a wait that ran out, the copies in flight still land.
-      if (!ok)
+      // After a wait that ran out, the copies in flight still land (a pair's
+      // second CTA stays until its first has seen that).
+      if (!ok && rank == 0)
         for (uint32_t i = it > S::STAGES ? it - S::STAGES : 0; i < it; ++i)
           mbar_wait_bounded(full + 8 * (i % S::STAGES), (i / S::STAGES) & 1, a.timeout_ns);
     }
     __syncwarp();
   } else if (warp == 9) {
-    // ---- tensor-core instructions ----
-    if (lane == 0) {
+    // ---- tensor-core instructions, from one thread ----
+    if (lane == 0 && rank == 0) {
       uint32_t it = 0, chunk = 0, acc = 0;
-      while (ok && walk.template next<BN>(a, tile)) {
+      while (ok && walk.next(a, tile)) {
         const int steps = (tile.depth + STEP_K - 1) / STEP_K;
         if (steps == 0) continue;
         // The accumulator's columns are free: for 256 columns, the shared 32
         // of the tile before (whose readers have then finished the tile
         // before that); otherwise, all of the tile two before.
         const uint32_t lag = BN == 256 ? 1 : 2;
-        if (acc >= lag && !mbar_wait_bounded(acc_empty + 8 * ((acc - lag) % 2),
-                                             ((acc - lag) / 2) & 1, a.timeout_ns)) {
+        if (acc >= lag && !mbar_wait_bounded_cluster(acc_empty + 8 * ((acc - lag) % 2),
+                                                     ((acc - lag) / 2) & 1, a.timeout_ns)) {
           ok = false;
           break;
         }
@@ -287,7 +335,8 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
         for (int k = 0; ok && k < steps; ++k, ++it) {
           const uint32_t c = chunk % S::SCALE_CHUNKS, s = it % S::STAGES;
           if (k % CHUNK == 0 &&
-              !mbar_wait_bounded(sc_full + 8 * c, (chunk / S::SCALE_CHUNKS) & 1, a.timeout_ns))
+              !mbar_wait_bounded_cluster(sc_full + 8 * c, (chunk / S::SCALE_CHUNKS) & 1,
+                                         a.timeout_ns))
             ok = false;
           if (!ok || !mbar_wait_bounded(full + 8 * s, (it / S::STAGES) & 1, a.timeout_ns)) {
             ok = false;
@@ -297,150 +346,215 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
           // Scales of this stage: A's tile, then B's, in alternating columns.
           const uint32_t sc = scales + c * S::SCALE_BYTES + (k % CHUNK) * 512;
           const uint32_t ts = tmem + SCALE_COL + (k % 2) * 16;
-          tc_copy_scales(ts, scale_desc(sc));
+          tc_copy_scales<CTAS>(ts, scale_desc(sc));
 #pragma unroll
           for (int b = 0; b < S::B_TILES; ++b)
-            tc_copy_scales(ts + 4 + 4 * b, scale_desc(sc + (1 + b) * CHUNK * 512));
+            tc_copy_scales<CTAS>(ts + 4 + 4 * b, scale_desc(sc + (1 + b) * CHUNK * 512));
           const uint64_t da = operand_desc(stages + s * S::STAGE_BYTES);
           const uint64_t db = operand_desc(stages + s * S::STAGE_BYTES + S::A_BYTES);
           const int left = (tile.depth - k * STEP_K) / 32;
 #pragma unroll
           for (int j = 0; j < STEP_K / 32; ++j)
             if (j < left)
-              tc_mma_mxf8(d, da + 2 * j, db + 2 * j, mxf8_idesc(TILE_M, BN, j), ts, ts + 4,
-                          k > 0 || j > 0);
-          tc_commit(empty + 8 * s);
+              tc_mma_mxf8<CTAS>(d, da + 2 * j, db + 2 * j, mxf8_idesc(ROWS * CTAS, BN, j), ts,
+                                ts + 4, k > 0 || j > 0);
+          tc_commit<CTAS>(empty + 8 * s);
           if (k % CHUNK == CHUNK - 1 || k == steps - 1) {
-            tc_commit(sc_empty + 8 * c);
+            tc_commit<CTAS>(sc_empty + 8 * c);
             ++chunk;
           }
         }
-        if (ok) tc_commit(acc_full + 8 * (acc % 2));
+        if (ok) tc_commit<CTAS>(acc_full + 8 * (acc % 2));
         ++acc;
       }
       // Nothing of this thread's is in flight when the memory is given back.
       if (!ok) {
-        tc_commit(drain);
+        tc_commit<CTAS>(drain);
         mbar_wait_bounded(drain, 0, a.timeout_ns);
       }
     }
     __syncwarp();
   } else if (warp >= 4) {
-    // ---- scales: thread r takes rows r of A and r, r + 128 of B ----
+    // ---- scales: thread r takes row r of this CTA's A rows and rows r,
+    // r + 128 of all of B, a chunk of 16 bytes each.  The loads run AHEAD
+    // chunks before the stores, over the ends of tiles too. ----
     const int r = tid - 128;
     const uint8_t* a_end = a.a_s + static_cast<int64_t>(WGRAD ? a.a_rows : a.limit) * a.s_ld;
     const uint8_t* b_end = a.b_s + (WGRAD ? 1 : a.groups) * static_cast<int64_t>(a.b_rows) * a.s_ld;
-    uint32_t chunk = 0;
-    while (ok && walk.template next<BN>(a, tile)) {
-      const int steps = (tile.depth + STEP_K - 1) / STEP_K;
-      const int blocks = tile.depth / 32;
-      const int64_t arow = (WGRAD ? 0 : off[tile.g]) + tile.m0 + r;
-      const bool ahas = tile.m0 + r < tile.rows;
-      const uint8_t* ap = a.a_s + arow * a.s_ld + tile.first / 32;
-      const uint8_t* bp = a.b_s +
-          ((WGRAD ? 0 : static_cast<int64_t>(tile.g) * a.b_rows) + tile.n0 + r) * a.s_ld +
-          tile.first / 32;
-      for (int k = 0; k < steps; k += CHUNK, ++chunk) {
-        const uint32_t c = chunk % S::SCALE_CHUNKS;
-        const int at = k * (STEP_K / 32), valid = blocks - at;
-        const uint4 va = load_scales(ap + at, ahas ? valid : 0, a_end);
-        uint4 vb[S::B_TILES];
+    uint4 v[AHEAD][1 + S::B_TILES];
+    const uint8_t *ap = nullptr, *bp = nullptr;
+    int blocks = 0, at = 0;          // of the tile being loaded
+    bool a_has = false;
+    auto load = [&](uint4 (&w)[1 + S::B_TILES]) {
+      while (at >= blocks) {
+        if (!walk.next(a, tile)) return false;
+        const int row = tile.m0 + static_cast<int>(rank) * ROWS + r;
+        blocks = tile.depth / 32;
+        at = 0;
+        a_has = row < tile.rows;
+        ap = a.a_s + ((WGRAD ? 0 : static_cast<int64_t>(off[tile.g])) + row) * a.s_ld +
+             tile.first / 32;
+        bp = a.b_s + ((WGRAD ? 0 : static_cast<int64_t>(tile.g) * a.b_rows) + tile.n0 + r) * a.s_ld +
+             tile.first / 32;
+      }
+      w[0] = load_scales(ap + at, a_has ? blocks - at : 0, a_end);
 #pragma unroll
-        for (int b = 0; b < S::B_TILES; ++b)
-          vb[b] = load_scales(bp + b * 128 * a.s_ld + at,
-                              tile.n0 + r + b * 128 < a.b_rows && r + b * 128 < BN ? valid : 0,
-                              b_end);
+      for (int b = 0; b < S::B_TILES; ++b)
+        w[1 + b] = load_scales(bp + b * 128 * a.s_ld + at,
+                               tile.n0 + r + b * 128 < a.b_rows && r + b * 128 < BN ? blocks - at : 0,
+                               b_end);
+      at += 16;
+      return true;
+    };
+    uint32_t chunk = 0, loaded = 0;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) loaded += load(v[i]);
+    while (ok && chunk < loaded) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (!ok || chunk >= loaded) break;
+        const uint32_t c = chunk % S::SCALE_CHUNKS;
         if (chunk >= S::SCALE_CHUNKS &&
             !mbar_wait_bounded(sc_empty + 8 * c, (chunk / S::SCALE_CHUNKS - 1) & 1, a.timeout_ns)) {
           ok = false;
           break;
         }
         const uint32_t dst = scales + c * S::SCALE_BYTES;
-        store_scales(dst, r, va);
 #pragma unroll
-        for (int b = 0; b < S::B_TILES; ++b) store_scales(dst + (1 + b) * CHUNK * 512, r, vb[b]);
+        for (int b = 0; b <= S::B_TILES; ++b) store_scales(dst + b * CHUNK * 512, r, v[i][b]);
         fence_proxy_async_smem();
-        mbar_arrive(sc_full + 8 * c);
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CTAS == 2) mbar_arrive_cluster(cluster_addr(sc_full + 8 * c, 0));
+          else mbar_arrive(sc_full + 8 * c);
+        }
+        ++chunk;
+        loaded += load(v[i]);
       }
     }
   } else {
     // ---- epilogue: warp w reads lanes 32 w .. 32 w + 31, a row each ----
+    const uint32_t patch = patches + warp * 4096;
     uint32_t acc = 0;
-    while (ok && walk.template next<BN>(a, tile)) {
-      const int row = tile.m0 + tid;
-      const bool live = row < tile.rows;
-      const int64_t out_row = WGRAD ? static_cast<int64_t>(tile.g) * a.a_rows + row
-                                    : static_cast<int64_t>(off[tile.g]) + row;
-      uint32_t v[32];
-      if (tile.depth == 0) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0;
-        for (int j = 0; j < BN; j += 32)
-          if (live) store_row(a, out_row, tile.n0 + j, a.b_rows - tile.n0 - j, v);
-        continue;
-      }
+    while (ok && walk.next(a, tile)) {
+      const int first = tile.m0 + static_cast<int>(rank) * ROWS + warp * 32;
+      const int rows = min(32, tile.rows - first);       // may be negative
+      const int64_t out_row = first + (WGRAD ? static_cast<int64_t>(tile.g) * a.a_rows
+                                             : static_cast<int64_t>(off[tile.g]));
       const uint32_t s = acc % 2;
-      if (!mbar_wait_bounded(acc_full + 8 * s, (acc / 2) & 1, a.timeout_ns)) {
-        ok = false;
-        break;
+      const bool empty_tile = tile.depth == 0;
+      if (!empty_tile) {
+        if (!mbar_wait_bounded(acc_full + 8 * s, (acc / 2) & 1, a.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        ++acc;
       }
-      tc_fence_after_sync();
       const uint32_t base = tmem + S::acc_col(s) + (static_cast<uint32_t>(warp) << 21);
-      for (int i = 0; i < BN / 32; ++i) {
+      const int width = a.out_f32 ? 32 : 64;             // columns of a patch
+      for (int i = 0; i < BN; i += width) {
         // Accumulator 0 shares its last 32 columns with the next tile's
         // first 32: they are read first.
-        const int j = 32 * (BN == 256 && s == 0 ? BN / 32 - 1 - i : i);
-        tmem_load_x32(base + j, v);
-        tmem_wait_load();
-        if (i == (BN == 256 ? 0 : BN / 32 - 1)) {
-          tc_fence_before_sync();
-          mbar_arrive(acc_empty + 8 * s);
+        const int j = BN == 256 && s == 0 ? BN - width - i : i;
+        __syncwarp();
+        for (int h = 0; h < width / 32; ++h) {
+          uint32_t v[32];
+          if (empty_tile) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] = 0;
+          } else {
+            tmem_load_x32(base + j + 32 * h, v);
+            tmem_wait_load();
+          }
+          const uint32_t line = patch + lane * 128;
+          if (a.out_f32) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              sts128(line + ((u ^ (lane & 7)) << 4), v[4 * u], v[4 * u + 1], v[4 * u + 2],
+                     v[4 * u + 3]);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t w[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                w[c] = pack_bf16(__uint_as_float(v[8 * u + 2 * c]),
+                                 __uint_as_float(v[8 * u + 2 * c + 1]));
+              sts128(line + (((4 * h + u) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+            }
+          }
         }
-        if (live) store_row(a, out_row, tile.n0 + j, a.b_rows - tile.n0 - j, v);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (!empty_tile && lane == 0 && i == (BN == 256 ? 0 : BN - width)) {
+          if constexpr (CTAS == 2) mbar_arrive_cluster(cluster_addr(acc_empty + 8 * s, 0));
+          else mbar_arrive(acc_empty + 8 * s);
+        }
+        store_patch(a, patch, lane, out_row, rows, tile.n0 + j, a.b_rows - tile.n0 - j, tile.add);
       }
-      ++acc;
     }
   }
 
   if (!ok && a.dev_err) atomicOr(a.dev_err, MXQ_DEVERR_TIMEOUT);
   tc_fence_before_sync();
   __syncthreads();
+  // A pair's CTAs leave together: each arrives on the other's barriers.
+  if constexpr (CTAS == 2) cluster_sync();
   tc_fence_after_sync();
-  if (warp == 9) tmem_dealloc(tmem, TMEM_COLS);
+  if (warp == 9) tmem_dealloc<CTAS>(tmem, TMEM_COLS);
 }
 
-template <int BN, bool WGRAD>
+template <int CTAS, int BN, bool WGRAD>
 cudaError_t launch(const GroupedMaps& maps, const GroupedArgs& a, int num_sms,
                    cudaStream_t stream) {
-  auto kernel = mx_grouped_kernel<BN, WGRAD>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Shape<BN>::SMEM);
+  auto kernel = mx_grouped_kernel<CTAS, BN, WGRAD>;
+  constexpr int smem = Shape<CTAS, BN>::SMEM;
+  static_assert(smem <= 227 * 1024, "shared memory of one SM");
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // At most this many tiles, whatever the offsets are.
+  constexpr int TILE_M = ROWS * CTAS;
   const int64_t tiles_n = (a.b_rows + BN - 1) / BN;
   const int64_t tiles_m =
       WGRAD ? static_cast<int64_t>(a.groups) * ((a.a_rows + TILE_M - 1) / TILE_M)
             : a.limit / TILE_M + (a.groups < a.limit ? a.groups : a.limit);
-  const int64_t tiles = tiles_m * tiles_n;
-  const int grid = static_cast<int>(tiles < num_sms ? tiles : num_sms);
-  kernel<<<grid, THREADS, Shape<BN>::SMEM, stream>>>(maps, a);
-  return cudaGetLastError();
+  const int64_t tiles = tiles_m * tiles_n, most = num_sms / CTAS;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles < most ? tiles : most) * CTAS);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = CTAS;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, a);
+}
+
+template <bool WGRAD>
+cudaError_t launch_plan(GroupedPlan plan, const GroupedMaps& maps, const GroupedArgs& a,
+                        int num_sms, cudaStream_t stream) {
+  if (plan.ctas == 2) return launch<2, 256, WGRAD>(maps, a, num_sms, stream);
+  return plan.cols == 256 ? launch<1, 256, WGRAD>(maps, a, num_sms, stream)
+                          : launch<1, 128, WGRAD>(maps, a, num_sms, stream);
 }
 
 }  // namespace
 
-int grouped_tile_cols(int64_t rows, int64_t cols, int groups, int num_sms) {
-  const int64_t tiles_m = rows / TILE_M + groups;
-  return tiles_m * ((cols + 255) / 256) >= 2 * num_sms ? 256 : 128;
+GroupedPlan grouped_plan(int64_t rows, int64_t cols, int groups, int num_sms) {
+  const int64_t tiles = (rows / ROWS + groups) * ((cols + 255) / 256);
+  if (rows >= static_cast<int64_t>(groups) * 2 * ROWS && tiles >= 2 * num_sms) return {2, 256};
+  return {1, tiles >= 2 * num_sms ? 256 : 128};
 }
 
 cudaError_t launch_grouped(const GroupedMaps& maps, const GroupedArgs& a, bool wgrad,
-                           int tile_cols, int num_sms, cudaStream_t stream) {
-  if (wgrad)
-    return tile_cols == 256 ? launch<256, true>(maps, a, num_sms, stream)
-                            : launch<128, true>(maps, a, num_sms, stream);
-  return tile_cols == 256 ? launch<256, false>(maps, a, num_sms, stream)
-                          : launch<128, false>(maps, a, num_sms, stream);
+                           GroupedPlan plan, int num_sms, cudaStream_t stream) {
+  return wgrad ? launch_plan<true>(plan, maps, a, num_sms, stream)
+               : launch_plan<false>(plan, maps, a, num_sms, stream);
 }
 
 }  // namespace mxq

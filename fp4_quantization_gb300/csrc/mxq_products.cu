@@ -73,15 +73,15 @@ mxq_status mx_grouped_gemm(const uint8_t* x_q, const uint8_t* x_s, const uint8_t
   a.s_ld = K / 32;
   a.dev_err = dev_err;
   a.timeout_ns = mxq::PRODUCT_TIMEOUT_NS;
-  const int cols = mxq::grouped_tile_cols(M, N, a.groups, sms);
+  const mxq::GroupedPlan plan = mxq::grouped_plan(M, N, a.groups, sms);
   mxq::GroupedMaps maps{};
   if (K > 0) {
     st = encode_codes(&maps.a, x_q, 1, M, K, 128, 2);
     if (st != MXQ_OK) return st;
-    st = encode_codes(&maps.b, w_q, E, N, K, cols, 3);
+    st = encode_codes(&maps.b, w_q, E, N, K, plan.box_rows(), 3);
     if (st != MXQ_OK) return st;
   }
-  return from_cuda(mxq::launch_grouped(maps, a, false, cols, sms, stream));
+  return from_cuda(mxq::launch_grouped(maps, a, false, plan, sms, stream));
 }
 
 mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, const uint8_t* x_q,
@@ -115,15 +115,15 @@ mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, const uint8_
   a.s_ld = M / 32;
   a.dev_err = dev_err;
   a.timeout_ns = mxq::PRODUCT_TIMEOUT_NS;
-  const int cols = mxq::grouped_tile_cols(N * E, K, a.groups, sms);
+  const mxq::GroupedPlan plan = mxq::grouped_plan(N * E, K, a.groups, sms);
   mxq::GroupedMaps maps{};
   if (M > 0) {
     st = encode_codes(&maps.a, g_q, 1, N, M, 128, 2);
     if (st != MXQ_OK) return st;
-    st = encode_codes(&maps.b, x_q, 1, K, M, cols, 3);
+    st = encode_codes(&maps.b, x_q, 1, K, M, plan.box_rows(), 3);
     if (st != MXQ_OK) return st;
   }
-  return from_cuda(mxq::launch_grouped(maps, a, true, cols, sms, stream));
+  return from_cuda(mxq::launch_grouped(maps, a, true, plan, sms, stream));
 }
 
 mxq_status nvfp4_gemv(const void* x, int64_t ldx, const uint8_t* w_q, const uint8_t* w_s,

@@ -11,7 +11,7 @@
 
 namespace mxq {
 
-constexpr int GROUPS_MAX = 1024;      // experts of one grouped call
+constexpr int GROUPS_MAX = 512;       // experts of one grouped call
 constexpr uint64_t PRODUCT_TIMEOUT_NS = 1000000000ull;   // 1 s per wait
 
 // One grouped product: tiles of out = A B^T, where A's and B's rows are codes
@@ -40,13 +40,21 @@ struct GroupedArgs {
 
 struct GroupedMaps {
   CUtensorMap a;            // 2-D codes, box 128 bytes x 128 rows, 128-byte swizzle
-  CUtensorMap b;            // 3-D codes (depth, row, group), box 128 bytes x tile columns x 1
+  CUtensorMap b;            // 3-D codes (depth, row, group), box 128 bytes x GroupedPlan::box_rows() x 1
 };
 
-// Columns of one output tile (B rows of one copy) for a call of this size.
-int grouped_tile_cols(int64_t rows, int64_t cols, int groups, int num_sms);
+// How a call's output is cut: tiles of 128 * ctas rows (a pair of CTAs works on
+// one where ctas is 2) and `cols` columns.
+struct GroupedPlan {
+  int ctas;
+  int cols;
+  int box_rows() const { return cols / ctas; }   // rows of one copy of B
+};
+
+// The plan for groups of rows / groups rows on average.
+GroupedPlan grouped_plan(int64_t rows, int64_t cols, int groups, int num_sms);
 cudaError_t launch_grouped(const GroupedMaps& maps, const GroupedArgs& a, bool wgrad,
-                           int tile_cols, int num_sms, cudaStream_t stream);
+                           GroupedPlan plan, int num_sms, cudaStream_t stream);
 
 struct GemvArgs {
   const uint16_t* x;        // bf16 [rows / share][ldx]

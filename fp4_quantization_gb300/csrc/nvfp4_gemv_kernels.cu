@@ -135,20 +135,6 @@ __device__ __forceinline__ void multiply_step(float (&acc)[TOKS / 8][4], const S
   }
 }
 
-// Cluster helpers: this CTA's rank along K, and a neighbour's shared memory.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-               ::: "memory");
-}
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
-  uint32_t at;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
-}
-
 // A CTA multiplies 16 * tiles weight rows by up to TOKS rows of x over its part
 // of K; its 8 warps are `tiles` row tiles x 8 / tiles parts of K (taken step
 // by step in turn).  The parts' sums are added through shared memory, and

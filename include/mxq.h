@@ -336,7 +336,7 @@ MXQ_API mxq_status nvfp4_quantize_transpose(const void* x, int64_t M, int64_t K,
  *   offsets [E + 1] int32 on the device, not decreasing, within [0, M]; a
  *           group may be empty, and rows in no group are not written.
  *           Offsets that break this set MXQ_DEVERR_OFFSETS in *dev_err and
- *           nothing is written.  E <= 1024.
+ *           nothing is written.  E <= 512.
  *   out     [M][ldo] bf16 or fp32, aligned to its element (16-byte aligned
  *           rows are written with wider stores); ldo >= N.
  *   K == 0 writes zeros; M, N or E == 0 is a valid empty call.

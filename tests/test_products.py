@@ -443,10 +443,10 @@ def test_grouped_refusals():
         return L.mx_grouped_wgrad(P, P, P, P, P, M, N, K, E, flags, P, None, None)
 
     assert gemm(flags=1) == 1 and wgrad(flags=512) == 1
-    for bad in (dict(M=-1), dict(N=-1), dict(K=-32), dict(K=40), dict(E=-1), dict(E=1025),
+    for bad in (dict(M=-1), dict(N=-1), dict(K=-32), dict(K=40), dict(E=-1), dict(E=513),
                 dict(M=2 ** 31), dict(ldo=63)):
         assert gemm(**bad) == 2, bad
-    for bad in (dict(M=-32), dict(M=48), dict(N=-1), dict(K=-1), dict(E=1025), dict(K=2 ** 31)):
+    for bad in (dict(M=-32), dict(M=48), dict(N=-1), dict(K=-1), dict(E=513), dict(K=2 ** 31)):
         assert wgrad(**bad) == 2, bad
 
 
