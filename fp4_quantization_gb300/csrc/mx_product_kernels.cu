@@ -213,7 +213,8 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
   const uint32_t drain = acc_empty + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(start + GROUPS_MAX + 1) + 2 * S::BARRIERS;
 
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, lane = tid % 32;
+  const int warp = __shfl_sync(~0u, tid / 32, 0);          // the same for the warp, known to be
   const int tiles_n = (a.b_rows + BN - 1) / BN;
   const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;   // 0: the CTA that issues
 
@@ -280,7 +281,7 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
 
   if (warp == 8) {
     // ---- copies: a stage of this CTA's rows of A and of B at a time ----
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t it = 0;
       while (ok && walk.next(a, tile)) {
         const int steps = (tile.depth + STEP_K - 1) / STEP_K;
@@ -316,7 +317,7 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
     __syncwarp();
   } else if (warp == 9) {
     // ---- tensor-core instructions, from one thread ----
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       uint32_t it = 0, chunk = 0, acc = 0;
       while (ok && walk.next(a, tile)) {
         const int steps = (tile.depth + STEP_K - 1) / STEP_K;

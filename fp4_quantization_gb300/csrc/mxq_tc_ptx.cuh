@@ -9,6 +9,19 @@
 
 namespace mxq {
 
+// One thread of a converged warp.  The compiler then knows that the branch has
+// one thread and issues tensor-core and copy instructions straight from uniform
+// registers: 128 clocks a 128 x 256 x 32 instruction, the tensor cores' own
+// rate, against 141 under `lane == 0`, and 95 against 141 for 128 x 128.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------------------
 // Tensor memory
 // ---------------------------------------------------------------------------
