@@ -14,8 +14,10 @@ namespace {
 
 constexpr int ROWS = 128;             // output rows of a CTA's tile
 constexpr int STEP_K = 128;           // contraction bytes of one pipeline stage: a swizzle row
-constexpr int CHUNK = 4;              // stages that share one set of scale tiles (16 bytes a row)
-constexpr int AHEAD = 2;              // chunks whose scales are on their way into registers
+// Stages whose scales are fetched together: 64 bytes a row, by four threads in
+// one request.  The scales are 3% of the bytes, but fetched 16 bytes at a time
+// they were 27% of the requests to L2, and the codes' copies waited for them.
+constexpr int CHUNK = 16;
 constexpr int THREADS = 320;          // 4 epilogue, 4 scale, 1 copy, 1 issuing warp
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t SCALE_COL = 480;   // first tensor-memory column of the scales
@@ -31,7 +33,7 @@ struct Shape {
   static constexpr int A_BYTES = ROWS * STEP_K;
   static constexpr int B_ROWS = BN / CTAS;                          // of each CTA
   static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * STEP_K;
-  static constexpr int STAGES = STAGE_BYTES > 40 * 1024 ? 4 : 5;
+  static constexpr int STAGES = STAGE_BYTES > 40 * 1024 ? 3 : 4;
   static constexpr int B_TILES = (BN + 127) / 128;                  // scale tiles of B a stage
   static constexpr int SCALE_BYTES = CHUNK * 512 * (1 + B_TILES);   // one scale chunk
   static constexpr int SCALE_CHUNKS = 2;
@@ -123,15 +125,6 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* p, int valid, const 
   const uint32_t bits = 8 * (shift & 3);
   return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
                     __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
-}
-
-// Writes row r's scales of the four stages of a chunk into their tiles.
-__device__ __forceinline__ void store_scales(uint32_t tiles, int r, uint4 v) {
-  const uint32_t at = tiles + (r % 32) * 16 + (r / 32) * 4;
-  sts32(at, v.x);
-  sts32(at + 512, v.y);
-  sts32(at + 1024, v.z);
-  sts32(at + 1536, v.w);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -376,62 +369,66 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
     }
     __syncwarp();
   } else if (warp >= 4) {
-    // ---- scales: thread r takes row r of this CTA's A rows and rows r,
-    // r + 128 of all of B, a chunk of 16 bytes each.  The loads run AHEAD
-    // chunks before the stores, over the ends of tiles too. ----
-    const int r = tid - 128;
+    // ---- scales: thread t takes piece t % 4 of rows t / 4 + 32 i of this
+    // CTA's A rows and of all of B's, so that a row's 64 bytes are one request,
+    // and a thread's rows one 16-byte unit of each stage's tile.  The loads run
+    // a chunk before the stores, over the ends of tiles too. ----
+    const int piece = tid % 4, r = (tid - 128) / 4;
     const uint8_t* a_end = a.a_s + static_cast<int64_t>(WGRAD ? a.a_rows : a.limit) * a.s_ld;
     const uint8_t* b_end = a.b_s + (WGRAD ? 1 : a.groups) * static_cast<int64_t>(a.b_rows) * a.s_ld;
-    uint4 v[AHEAD][1 + S::B_TILES];
+    uint4 v[1 + S::B_TILES][4];
     const uint8_t *ap = nullptr, *bp = nullptr;
     int blocks = 0, at = 0;          // of the tile being loaded
-    bool a_has = false;
-    auto load = [&](uint4 (&w)[1 + S::B_TILES]) {
+    int a_left = 0, b_left = 0;      // rows from r on that exist
+    auto load = [&] {
       while (at >= blocks) {
         if (!walk.next(a, tile)) return false;
         const int row = tile.m0 + static_cast<int>(rank) * ROWS + r;
         blocks = tile.depth / 32;
         at = 0;
-        a_has = row < tile.rows;
+        a_left = tile.rows - row;
+        b_left = a.b_rows - tile.n0 - r;
         ap = a.a_s + ((WGRAD ? 0 : static_cast<int64_t>(off[tile.g])) + row) * a.s_ld +
-             tile.first / 32;
+             tile.first / 32 + 16 * piece;
         bp = a.b_s + ((WGRAD ? 0 : static_cast<int64_t>(tile.g) * a.b_rows) + tile.n0 + r) * a.s_ld +
-             tile.first / 32;
+             tile.first / 32 + 16 * piece;
       }
-      w[0] = load_scales(ap + at, a_has ? blocks - at : 0, a_end);
+      const int valid = blocks - at - 16 * piece;
 #pragma unroll
-      for (int b = 0; b < S::B_TILES; ++b)
-        w[1 + b] = load_scales(bp + b * 128 * a.s_ld + at,
-                               tile.n0 + r + b * 128 < a.b_rows && r + b * 128 < BN ? blocks - at : 0,
-                               b_end);
-      at += 16;
+      for (int i = 0; i < 4; ++i) {
+        v[0][i] = load_scales(ap + i * 32 * a.s_ld + at, 32 * i < a_left ? valid : 0, a_end);
+#pragma unroll
+        for (int b = 0; b < S::B_TILES; ++b)
+          v[1 + b][i] = load_scales(bp + (b * 128 + i * 32) * a.s_ld + at,
+                                    b * 128 + 32 * i < b_left ? valid : 0, b_end);
+      }
+      at += 64;
       return true;
     };
-    uint32_t chunk = 0, loaded = 0;
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) loaded += load(v[i]);
-    while (ok && chunk < loaded) {
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        if (!ok || chunk >= loaded) break;
-        const uint32_t c = chunk % S::SCALE_CHUNKS;
-        if (chunk >= S::SCALE_CHUNKS &&
-            !mbar_wait_bounded(sc_empty + 8 * c, (chunk / S::SCALE_CHUNKS - 1) & 1, a.timeout_ns)) {
-          ok = false;
-          break;
-        }
-        const uint32_t dst = scales + c * S::SCALE_BYTES;
-#pragma unroll
-        for (int b = 0; b <= S::B_TILES; ++b) store_scales(dst + b * CHUNK * 512, r, v[i][b]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CTAS == 2) mbar_arrive_cluster(cluster_addr(sc_full + 8 * c, 0));
-          else mbar_arrive(sc_full + 8 * c);
-        }
-        ++chunk;
-        loaded += load(v[i]);
+    uint32_t chunk = 0;
+    for (bool more = load(); more; ++chunk) {
+      const uint32_t c = chunk % S::SCALE_CHUNKS;
+      if (chunk >= S::SCALE_CHUNKS &&
+          !mbar_wait_bounded(sc_empty + 8 * c, (chunk / S::SCALE_CHUNKS - 1) & 1, a.timeout_ns)) {
+        ok = false;
+        break;
       }
+      const uint32_t dst = scales + c * S::SCALE_BYTES + piece * 2048 + r * 16;
+#pragma unroll
+      for (int b = 0; b <= S::B_TILES; ++b) {
+        const uint32_t to = dst + b * CHUNK * 512;
+        sts128(to, v[b][0].x, v[b][1].x, v[b][2].x, v[b][3].x);
+        sts128(to + 512, v[b][0].y, v[b][1].y, v[b][2].y, v[b][3].y);
+        sts128(to + 1024, v[b][0].z, v[b][1].z, v[b][2].z, v[b][3].z);
+        sts128(to + 1536, v[b][0].w, v[b][1].w, v[b][2].w, v[b][3].w);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CTAS == 2) mbar_arrive_cluster(cluster_addr(sc_full + 8 * c, 0));
+        else mbar_arrive(sc_full + 8 * c);
+      }
+      more = load();
     }
   } else {
     // ---- epilogue: warp w reads lanes 32 w .. 32 w + 31, a row each ----
