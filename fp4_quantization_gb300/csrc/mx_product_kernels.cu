@@ -37,7 +37,10 @@ struct Shape {
   static constexpr int B_TILES = (BN + 127) / 128;                  // scale tiles of B a stage
   static constexpr int SCALE_BYTES = CHUNK * 512 * (1 + B_TILES);   // one scale chunk
   static constexpr int SCALE_CHUNKS = 2;
-  static constexpr int OUT_BYTES = 4 * 32 * 128;                    // a 32-row x 128-byte patch a warp
+  // Patches of 32 rows x 128 bytes that the epilogue's four warps stage: two
+  // each, one filled while the other leaves (one where shared memory is short).
+  static constexpr int PATCHES = STAGE_BYTES > 40 * 1024 ? 1 : 2;
+  static constexpr int OUT_BYTES = 4 * PATCHES * 4096;
   // Column of accumulator s.  Two 256-column accumulators share 32 columns.
   static constexpr uint32_t acc_col(uint32_t s) { return s * (BN == 256 ? 224 : BN); }
   static constexpr int TABLE_BYTES = 2 * (GROUPS_MAX + 1) * 4;
@@ -47,12 +50,21 @@ struct Shape {
 };
 
 // Where a tile lies: its group, its first row and column in the group's
-// output, and the group's rows and the tile's contraction range.
+// output, the group's rows, and the tile's contraction range.
 struct Tile {
   int g, m0, n0;
   int rows;         // rows of the group's output
-  int first, depth; // contraction range
-  bool add;         // to what an earlier range of the same tile has written
+  int first, end;   // contraction range
+  bool part;        // one of several ranges whose sums are added
+  bool add;         // to what an earlier range has written
+
+  // Stages start on whole swizzle rows, so that their scales are whole words
+  // and, where scale rows are multiples of 16 bytes, chunks whole 64-byte
+  // pieces of them; the blocks of 32 before `first` are skipped.
+  __device__ __forceinline__ int step0() const { return first / STEP_K; }
+  __device__ __forceinline__ int step1() const {
+    return first < end ? (end + STEP_K - 1) / STEP_K : step0();
+  }
 };
 
 // Walks the tiles of this CTA (or pair) in order.  Inside a group the row
@@ -63,18 +75,19 @@ struct Walk {
   const int* off;
   const int* start;     // first tile of each group, and the total
   int groups, tiles_n;
-  int t, g, done;       // done: contraction values of tile t that are behind
+  int t, g, done;       // done: where tile t's next contraction range starts, or 0
 
   __device__ __forceinline__ bool next(const GroupedArgs& a, Tile& tile) {
     if (t >= start[groups]) return false;
     while (t >= start[g + 1]) ++g;
     const int lo = off[g], rows_g = off[g + 1] - lo;
-    const int whole = WGRAD ? rows_g : a.depth;
     tile.g = g;
     tile.rows = WGRAD ? a.a_rows : rows_g;
-    tile.first = (WGRAD ? lo : 0) + done;
-    tile.depth = a.out_f32 ? min(whole - done, SEGMENT) : whole;
+    const int from = WGRAD ? lo : 0, to = WGRAD ? lo + rows_g : a.depth;
     tile.add = done > 0;
+    tile.first = tile.add ? done : from;
+    tile.end = a.out_f32 ? min(to, (tile.first / STEP_K + SEGMENT / STEP_K) * STEP_K) : to;
+    tile.part = tile.add || tile.end < to;
     constexpr int BAND = 2048 / (ROWS * CTAS);
     const int tiles_m = (tile.rows + ROWS * CTAS - 1) / (ROWS * CTAS);
     int i = t - start[g];
@@ -83,8 +96,8 @@ struct Walk {
     const int height = min(BAND, tiles_m - band * BAND);
     tile.m0 = (band * BAND + i % height) * (ROWS * CTAS);
     tile.n0 = i / height * BN;
-    done += tile.depth;
-    if (done == whole) {
+    done = tile.end;
+    if (done == to) {
       done = 0;
       t += gridDim.x / CTAS;
     }
@@ -277,11 +290,10 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
     if (elect_one()) {
       uint32_t it = 0;
       while (ok && walk.next(a, tile)) {
-        const int steps = (tile.depth + STEP_K - 1) / STEP_K;
         const int ay = (WGRAD ? 0 : off[tile.g]) + tile.m0 + static_cast<int>(rank) * ROWS;
         const int by = tile.n0 + static_cast<int>(rank) * S::B_ROWS;
         const int bz = WGRAD ? 0 : tile.g;
-        for (int k = 0; k < steps; ++k, ++it) {
+        for (int k = tile.step0(); k < tile.step1(); ++k, ++it) {
           const uint32_t s = it % S::STAGES;
           if (it >= S::STAGES &&
               !mbar_wait_bounded(empty + 8 * s, (it / S::STAGES - 1) & 1, a.timeout_ns)) {
@@ -290,7 +302,7 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
           }
           const uint32_t dst = stages + s * S::STAGE_BYTES, bar = full + 8 * s;
           if (rank == 0) mbar_arrive_expect_tx(bar, CTAS * S::STAGE_BYTES);
-          const int x = tile.first + k * STEP_K;
+          const int x = k * STEP_K;
           if constexpr (CTAS == 2) {
             const uint32_t there = cluster_addr(bar, 0);
             tma_load_2d_pair(dst, &maps.a, x, ay, there);
@@ -313,8 +325,8 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
     if (rank == 0 && elect_one()) {
       uint32_t it = 0, chunk = 0, acc = 0;
       while (ok && walk.next(a, tile)) {
-        const int steps = (tile.depth + STEP_K - 1) / STEP_K;
-        if (steps == 0) continue;
+        const int k0 = tile.step0(), k1 = tile.step1();
+        if (k0 == k1) continue;
         // The accumulator's columns are free: for 256 columns, the shared 32
         // of the tile before (whose readers have then finished the tile
         // before that); otherwise, all of the tile two before.
@@ -326,9 +338,10 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
         }
         tc_fence_after_sync();
         const uint32_t d = tmem + S::acc_col(acc % 2);
-        for (int k = 0; ok && k < steps; ++k, ++it) {
+        bool accumulate = false;
+        for (int k = k0; ok && k < k1; ++k, ++it) {
           const uint32_t c = chunk % S::SCALE_CHUNKS, s = it % S::STAGES;
-          if (k % CHUNK == 0 &&
+          if ((k == k0 || k % CHUNK == 0) &&
               !mbar_wait_bounded_cluster(sc_full + 8 * c, (chunk / S::SCALE_CHUNKS) & 1,
                                          a.timeout_ns))
             ok = false;
@@ -346,14 +359,16 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
             tc_copy_scales<CTAS>(ts + 4 + 4 * b, scale_desc(sc + (1 + b) * CHUNK * 512));
           const uint64_t da = operand_desc(stages + s * S::STAGE_BYTES);
           const uint64_t db = operand_desc(stages + s * S::STAGE_BYTES + S::A_BYTES);
-          const int left = (tile.depth - k * STEP_K) / 32;
+          const int j0 = (tile.first - k * STEP_K) / 32, j1 = (tile.end - k * STEP_K) / 32;
 #pragma unroll
           for (int j = 0; j < STEP_K / 32; ++j)
-            if (j < left)
+            if (j >= j0 && j < j1) {
               tc_mma_mxf8<CTAS>(d, da + 2 * j, db + 2 * j, mxf8_idesc(ROWS * CTAS, BN, j), ts,
-                                ts + 4, k > 0 || j > 0);
+                                ts + 4, accumulate);
+              accumulate = true;
+            }
           tc_commit<CTAS>(empty + 8 * s);
-          if (k % CHUNK == CHUNK - 1 || k == steps - 1) {
+          if (k % CHUNK == CHUNK - 1 || k == k1 - 1) {
             tc_commit<CTAS>(sc_empty + 8 * c);
             ++chunk;
           }
@@ -378,22 +393,22 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
     const uint8_t* b_end = a.b_s + (WGRAD ? 1 : a.groups) * static_cast<int64_t>(a.b_rows) * a.s_ld;
     uint4 v[1 + S::B_TILES][4];
     const uint8_t *ap = nullptr, *bp = nullptr;
-    int blocks = 0, at = 0;          // of the tile being loaded
+    int at = 0, end = 0;             // scale bytes of the tile being loaded
     int a_left = 0, b_left = 0;      // rows from r on that exist
     auto load = [&] {
-      while (at >= blocks) {
+      while (at >= end) {
         if (!walk.next(a, tile)) return false;
         const int row = tile.m0 + static_cast<int>(rank) * ROWS + r;
-        blocks = tile.depth / 32;
-        at = 0;
+        at = tile.step0() / CHUNK * (CHUNK * 4);
+        end = tile.first < tile.end ? tile.end / 32 : at;
         a_left = tile.rows - row;
         b_left = a.b_rows - tile.n0 - r;
-        ap = a.a_s + ((WGRAD ? 0 : static_cast<int64_t>(off[tile.g])) + row) * a.s_ld +
-             tile.first / 32 + 16 * piece;
+        ap = a.a_s + ((WGRAD ? 0 : static_cast<int64_t>(off[tile.g])) + row) * a.s_ld + 16 * piece;
         bp = a.b_s + ((WGRAD ? 0 : static_cast<int64_t>(tile.g) * a.b_rows) + tile.n0 + r) * a.s_ld +
-             tile.first / 32 + 16 * piece;
+             16 * piece;
       }
-      const int valid = blocks - at - 16 * piece;
+      // Pieces before the range are skipped like those after it.
+      const int valid = at + 16 * piece + 16 > tile.first / 32 ? end - at - 16 * piece : 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[0][i] = load_scales(ap + i * 32 * a.s_ld + at, 32 * i < a_left ? valid : 0, a_end);
@@ -402,7 +417,7 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
           v[1 + b][i] = load_scales(bp + (b * 128 + i * 32) * a.s_ld + at,
                                     b * 128 + 32 * i < b_left ? valid : 0, b_end);
       }
-      at += 64;
+      at += CHUNK * 4;
       return true;
     };
     uint32_t chunk = 0;
@@ -432,15 +447,17 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
     }
   } else {
     // ---- epilogue: warp w reads lanes 32 w .. 32 w + 31, a row each ----
-    const uint32_t patch = patches + warp * 4096;
-    uint32_t acc = 0;
+    uint32_t acc = 0, turn = 0;
     while (ok && walk.next(a, tile)) {
       const int first = tile.m0 + static_cast<int>(rank) * ROWS + warp * 32;
       const int rows = min(32, tile.rows - first);       // may be negative
       const int64_t out_row = first + (WGRAD ? static_cast<int64_t>(tile.g) * a.a_rows
                                              : static_cast<int64_t>(off[tile.g]));
       const uint32_t s = acc % 2;
-      const bool empty_tile = tile.depth == 0;
+      const bool empty_tile = tile.first == tile.end;
+      // Whole patches leave by bulk copies, clipped at the output's last column;
+      // those with rows of the next group, and sums to be added, by threads.
+      const bool bulk = a.out_vec && !tile.part && (WGRAD ? rows > 0 : rows == 32);
       if (!empty_tile) {
         if (!mbar_wait_bounded(acc_full + 8 * s, (acc / 2) & 1, a.timeout_ns)) {
           ok = false;
@@ -455,6 +472,8 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
         // Accumulator 0 shares its last 32 columns with the next tile's
         // first 32: they are read first.
         const int j = BN == 256 && s == 0 ? BN - width - i : i;
+        const uint32_t patch = patches + (warp * S::PATCHES + turn++ % S::PATCHES) * 4096;
+        if (lane == 0) bulk_wait_read<S::PATCHES - 1>();
         __syncwarp();
         for (int h = 0; h < width / 32; ++h) {
           uint32_t v[32];
@@ -483,15 +502,24 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
             }
           }
         }
+        fence_proxy_async_smem();
         tc_fence_before_sync();
         __syncwarp();
         if (!empty_tile && lane == 0 && i == (BN == 256 ? 0 : BN - width)) {
           if constexpr (CTAS == 2) mbar_arrive_cluster(cluster_addr(acc_empty + 8 * s, 0));
           else mbar_arrive(acc_empty + 8 * s);
         }
-        store_patch(a, patch, lane, out_row, rows, tile.n0 + j, a.b_rows - tile.n0 - j, tile.add);
+        if (!bulk) {
+          store_patch(a, patch, lane, out_row, rows, tile.n0 + j, a.b_rows - tile.n0 - j,
+                      tile.add);
+        } else if (lane == 0 && tile.n0 + j < a.b_rows) {
+          tma_store_3d(&maps.out, patch, tile.n0 + j, WGRAD ? first : static_cast<int>(out_row),
+                       WGRAD ? tile.g : 0);
+        }
+        if (lane == 0) bulk_commit();       // one group a patch, empty ones too
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   if (!ok && a.dev_err) atomicOr(a.dev_err, MXQ_DEVERR_TIMEOUT);

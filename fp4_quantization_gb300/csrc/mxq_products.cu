@@ -27,15 +27,26 @@ mxq_status encode_codes(CUtensorMap* map, const uint8_t* q, int64_t groups, int6
                          CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Sets the output fields after checking them: `width` columns a row.
-mxq_status set_output(mxq::GroupedArgs* a, void* out, int64_t ldo, uint32_t flags) {
+// Sets the output fields after checking them: [groups][rows][cols], ldo
+// elements between rows.
+mxq_status set_output(mxq::GroupedArgs* a, CUtensorMap* map, void* out, int64_t groups,
+                      int64_t rows, int64_t cols, int64_t ldo, uint32_t flags) {
   const int size = (flags & MXQ_OUT_F32) ? 4 : 2;
   if (!aligned(out, size)) return MXQ_EALIGN;
   a->out = out;
   a->ldo = ldo;
   a->out_f32 = size == 4;
   a->out_vec = aligned(out, 16) && (ldo * size) % 16 == 0;
-  return MXQ_OK;
+  if (!a->out_vec) return MXQ_OK;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(groups)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ldo * size),
+                                 static_cast<cuuint64_t>(ldo * size * rows)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), 32, 1};
+  return mxq::encode_map(map,
+                         size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                         3, out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
@@ -61,7 +72,8 @@ mxq_status mx_grouped_gemm(const uint8_t* x_q, const uint8_t* x_s, const uint8_t
       !aligned(offsets, 4))
     return MXQ_EALIGN;
   mxq::GroupedArgs a{};
-  st = set_output(&a, out, ldo, flags);
+  mxq::GroupedMaps maps{};
+  st = set_output(&a, &maps.out, out, 1, M, N, ldo, flags);
   if (st != MXQ_OK) return st;
   a.offsets = offsets;
   a.groups = static_cast<int>(E);
@@ -74,7 +86,6 @@ mxq_status mx_grouped_gemm(const uint8_t* x_q, const uint8_t* x_s, const uint8_t
   a.dev_err = dev_err;
   a.timeout_ns = mxq::PRODUCT_TIMEOUT_NS;
   const mxq::GroupedPlan plan = mxq::grouped_plan(M, N, a.groups, sms);
-  mxq::GroupedMaps maps{};
   if (K > 0) {
     st = encode_codes(&maps.a, x_q, 1, M, K, 128, 2);
     if (st != MXQ_OK) return st;
@@ -103,7 +114,8 @@ mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, const uint8_
       !aligned(offsets, 4))
     return MXQ_EALIGN;
   mxq::GroupedArgs a{};
-  st = set_output(&a, dw, K, flags);
+  mxq::GroupedMaps maps{};
+  st = set_output(&a, &maps.out, dw, E, N, K, K, flags);
   if (st != MXQ_OK) return st;
   a.offsets = offsets;
   a.groups = static_cast<int>(E);
@@ -116,7 +128,6 @@ mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, const uint8_
   a.dev_err = dev_err;
   a.timeout_ns = mxq::PRODUCT_TIMEOUT_NS;
   const mxq::GroupedPlan plan = mxq::grouped_plan(N * E, K, a.groups, sms);
-  mxq::GroupedMaps maps{};
   if (M > 0) {
     st = encode_codes(&maps.a, g_q, 1, N, M, 128, 2);
     if (st != MXQ_OK) return st;

@@ -41,6 +41,8 @@ struct GroupedArgs {
 struct GroupedMaps {
   CUtensorMap a;            // 2-D codes, box 128 bytes x 128 rows, 128-byte swizzle
   CUtensorMap b;            // 3-D codes (depth, row, group), box 128 bytes x GroupedPlan::box_rows() x 1
+  CUtensorMap out;          // 3-D output (column, row, group), box 128 bytes x 32 rows x 1, 128-byte
+                            // swizzle; unset unless GroupedArgs::out_vec
 };
 
 // How a call's output is cut: tiles of 128 * ctas rows (a pair of CTAs works on
