@@ -313,31 +313,52 @@ def nvfp4_quantize_transpose(x, flags=ROWWISE | COLWISE, *, amax=None, global_sc
 
 
 _OUT_FLAGS = {torch.bfloat16: 0, torch.float32: OUT_F32}
+_U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
 
 
-def _operand(t, name, dim, dtype=torch.uint8):
+# The products' calls take microseconds on the GPU, so their bindings look at
+# each tensor once and cheaply, and say what is wrong only once something is.
+def _operand(t, name, dim, dtype=_U8):
+    """Shape of a contiguous CUDA tensor of this type and rank."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        shape = t.shape
+        if len(shape) == dim:
+            return shape
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dim:
         raise TypeError(f"{name} must be a {dim}-D {dtype} tensor")
     if not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.shape
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _product_out(out, shape, out_dtype, device):
+def _product_out(out, shape, out_dtype, like):
     """The output tensor (allocated when not given), its row stride and the
     flags of its type."""
     if out is None:
-        out = _empty(shape, out_dtype, device)
-    elif tuple(out.shape) != shape or not out.is_cuda:
+        flags = _OUT_FLAGS.get(out_dtype)
+        if flags is None:
+            raise TypeError("the output type is torch.bfloat16 or torch.float32")
+        return like.new_empty(shape, dtype=out_dtype), max(shape[-1], 1), flags
+    if tuple(out.shape) != shape or not out.is_cuda:
         raise ValueError(f"out must be a CUDA tensor of shape {shape}")
     if out.dtype not in _OUT_FLAGS:
         raise TypeError("the output type is torch.bfloat16 or torch.float32")
     if shape[-1] > 1 and out.stride(-1) != 1:
         raise ValueError("out needs a unit column stride")
-    ldo = out.stride(-2) if shape[-2] > 1 else max(shape[-1], 1)
-    return out, ldo, _OUT_FLAGS[out.dtype]
+    return out, out.stride(-2) if shape[-2] > 1 else max(shape[-1], 1), _OUT_FLAGS[out.dtype]
+
+
+def _err_ptr(dev_err):
+    return None if dev_err is None else dev_err.data_ptr()
+
+
+def _raw_stream(stream, like):
+    """The cudaStream_t of `stream`, or of the current stream of the tensor's
+    device (as a number; torch.cuda.current_stream() builds an object first,
+    3 us)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(like.get_device())
 
 
 def mx_grouped_gemm(x_q, x_s, w_q, w_s, offsets, *, out=None, out_dtype=torch.bfloat16,
@@ -349,15 +370,15 @@ def mx_grouped_gemm(x_q, x_s, w_q, w_s, offsets, *, out=None, out_dtype=torch.bf
     pass the gradient's rows and the weights' COLWISE codes [E,K,N]."""
     M, K = _operand(x_q, "x_q", 2)
     E, N, Kw = _operand(w_q, "w_q", 3)
-    if Kw != K or tuple(_operand(x_s, "x_s", 2)) != (M, K // 32) \
-            or tuple(_operand(w_s, "w_s", 3)) != (E, N, K // 32):
+    if Kw != K or _operand(x_s, "x_s", 2) != (M, K // 32) \
+            or _operand(w_s, "w_s", 3) != (E, N, K // 32):
         raise ValueError("x_q [M,K], x_s [M,K/32], w_q [E,N,K] and w_s [E,N,K/32] do not agree")
-    if tuple(_operand(offsets, "offsets", 1, torch.int32)) != (E + 1,):
+    if _operand(offsets, "offsets", 1, _I32) != (E + 1,):
         raise ValueError("offsets must have one entry more than there are experts")
-    out, ldo, flags = _product_out(out, (M, N), out_dtype, x_q.device)
+    out, ldo, flags = _product_out(out, (M, N), out_dtype, x_q)
     st = _lib.lib().mx_grouped_gemm(
         x_q.data_ptr(), x_s.data_ptr(), w_q.data_ptr(), w_s.data_ptr(), offsets.data_ptr(), M, N,
-        K, E, flags, out.data_ptr(), ldo, _ptr(dev_err), _stream(stream))
+        K, E, flags, out.data_ptr(), ldo, _err_ptr(dev_err), _raw_stream(stream, x_q))
     _check(st, "mx_grouped_gemm")
     return out
 
@@ -370,18 +391,18 @@ def mx_grouped_wgrad(g_q, g_s, x_q, x_s, offsets, *, out=None, out_dtype=torch.f
     bf16."""
     N, M = _operand(g_q, "g_q", 2)
     K, Mx = _operand(x_q, "x_q", 2)
-    if Mx != M or tuple(_operand(g_s, "g_s", 2)) != (N, M // 32) \
-            or tuple(_operand(x_s, "x_s", 2)) != (K, M // 32):
+    if Mx != M or _operand(g_s, "g_s", 2) != (N, M // 32) \
+            or _operand(x_s, "x_s", 2) != (K, M // 32):
         raise ValueError("g_q [N,M], g_s [N,M/32], x_q [K,M] and x_s [K,M/32] do not agree")
-    E = _operand(offsets, "offsets", 1, torch.int32)[0] - 1
+    E = _operand(offsets, "offsets", 1, _I32)[0] - 1
     if E < 0:
         raise ValueError("offsets must have one entry more than there are experts")
-    out, _, flags = _product_out(out, (E, N, K), out_dtype, g_q.device)
+    out, _, flags = _product_out(out, (E, N, K), out_dtype, g_q)
     if not out.is_contiguous():
         raise ValueError("out must be contiguous")
     st = _lib.lib().mx_grouped_wgrad(
         g_q.data_ptr(), g_s.data_ptr(), x_q.data_ptr(), x_s.data_ptr(), offsets.data_ptr(), M, N,
-        K, E, flags, out.data_ptr(), _ptr(dev_err), _stream(stream))
+        K, E, flags, out.data_ptr(), _err_ptr(dev_err), _raw_stream(stream, g_q))
     _check(st, "mx_grouped_wgrad")
     return out
 
@@ -396,21 +417,23 @@ def nvfp4_gemv(x, w_q, w_s, global_scale, *, experts=None, share=1, out=None,
     bf16 or fp32."""
     ldx = _input(x)
     T, K = x.shape
-    dim = 2 if experts is None else 3
-    N = _operand(w_q, "w_q", dim)[-2]
-    E = 1 if experts is None else w_q.shape[0]
-    lead = () if experts is None else (E,)
-    if K % 2 or tuple(w_q.shape) != lead + (N, K // 2) \
-            or tuple(_operand(w_s, "w_s", dim)) != lead + (N, K // 16):
+    if experts is None:
+        E, lead, ids = 1, (), None
+        N = _operand(w_q, "w_q", 2)[0]
+    else:
+        E, N, _ = _operand(w_q, "w_q", 3)
+        lead, ids = (E,), experts.data_ptr()
+        if _operand(experts, "experts", 1, _I32) != (T * share,):
+            raise ValueError("experts must have T * share entries")
+    if K % 2 or w_q.shape != lead + (N, K // 2) \
+            or _operand(w_s, "w_s", len(lead) + 2) != lead + (N, K // 16):
         raise ValueError("x [T,K], w_q [(E,) N,K/2] and w_s [(E,) N,K/16] do not agree")
-    if _operand(global_scale, "global_scale", 1, torch.float32)[0] != E:
+    if _operand(global_scale, "global_scale", 1, _F32) != (E,):
         raise ValueError("global_scale must have one entry for each expert")
-    if experts is not None and tuple(_operand(experts, "experts", 1, torch.int32)) != (T * share,):
-        raise ValueError("experts must have T * share entries")
-    out, ldo, flags = _product_out(out, (T * share, N), out_dtype, x.device)
+    out, ldo, flags = _product_out(out, (T * share, N), out_dtype, x)
     st = _lib.lib().nvfp4_gemv(
-        x.data_ptr(), ldx, w_q.data_ptr(), w_s.data_ptr(), global_scale.data_ptr(),
-        _ptr(experts), T, share, N, K, E, flags, out.data_ptr(), ldo, _stream(stream))
+        x.data_ptr(), ldx, w_q.data_ptr(), w_s.data_ptr(), global_scale.data_ptr(), ids, T, share,
+        N, K, E, flags, out.data_ptr(), ldo, _raw_stream(stream, x))
     _check(st, "nvfp4_gemv")
     return out
 

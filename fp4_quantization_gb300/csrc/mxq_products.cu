@@ -85,7 +85,7 @@ mxq_status mx_grouped_gemm(const uint8_t* x_q, const uint8_t* x_s, const uint8_t
   a.s_ld = K / 32;
   a.dev_err = dev_err;
   a.timeout_ns = mxq::PRODUCT_TIMEOUT_NS;
-  const mxq::GroupedPlan plan = mxq::grouped_plan(M, N, a.groups, sms);
+  const mxq::GroupedPlan plan = mxq::grouped_plan(M, N, K, a.groups, sms);
   if (K > 0) {
     st = encode_codes(&maps.a, x_q, 1, M, K, 128, 2);
     if (st != MXQ_OK) return st;
@@ -127,7 +127,7 @@ mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, const uint8_
   a.s_ld = M / 32;
   a.dev_err = dev_err;
   a.timeout_ns = mxq::PRODUCT_TIMEOUT_NS;
-  const mxq::GroupedPlan plan = mxq::grouped_plan(N * E, K, a.groups, sms);
+  const mxq::GroupedPlan plan = mxq::grouped_plan(N * E, K, M / E, a.groups, sms);
   if (M > 0) {
     st = encode_codes(&maps.a, g_q, 1, N, M, 128, 2);
     if (st != MXQ_OK) return st;

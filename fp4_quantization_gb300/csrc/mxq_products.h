@@ -53,8 +53,9 @@ struct GroupedPlan {
   int box_rows() const { return cols / ctas; }   // rows of one copy of B
 };
 
-// The plan for groups of rows / groups rows on average.
-GroupedPlan grouped_plan(int64_t rows, int64_t cols, int groups, int num_sms);
+// The plan for groups of rows / groups output rows on average, whose elements
+// are sums of `depth` products.
+GroupedPlan grouped_plan(int64_t rows, int64_t cols, int64_t depth, int groups, int num_sms);
 cudaError_t launch_grouped(const GroupedMaps& maps, const GroupedArgs& a, bool wgrad,
                            GroupedPlan plan, int num_sms, cudaStream_t stream);
 
