@@ -338,7 +338,7 @@ def _product_out(out, shape, out_dtype, like):
         flags = _OUT_FLAGS.get(out_dtype)
         if flags is None:
             raise TypeError("the output type is torch.bfloat16 or torch.float32")
-        return like.new_empty(shape, dtype=out_dtype), max(shape[-1], 1), flags
+        return torch.empty(shape, dtype=out_dtype, device=like.device), max(shape[-1], 1), flags
     if tuple(out.shape) != shape or not out.is_cuda:
         raise ValueError(f"out must be a CUDA tensor of shape {shape}")
     if out.dtype not in _OUT_FLAGS:
@@ -408,7 +408,7 @@ def mx_grouped_wgrad(g_q, g_s, x_q, x_s, offsets, *, out=None, out_dtype=torch.f
 
 
 def nvfp4_gemv(x, w_q, w_s, global_scale, *, experts=None, share=1, out=None,
-               out_dtype=torch.bfloat16, stream=None):
+               out_dtype=torch.bfloat16, dev_err=None, stream=None):
     """Few rows times NVFP4 weights as nvfp4_quantize_transpose writes them
     (ROWWISE): x [T,K] bf16 with w_q [N,K/2] / w_s [N,K/16] / global_scale
     [1], or with experts [T*share] int32 and w_q [E,N,K/2] / w_s [E,N,K/16] /
@@ -433,7 +433,7 @@ def nvfp4_gemv(x, w_q, w_s, global_scale, *, experts=None, share=1, out=None,
     out, ldo, flags = _product_out(out, (T * share, N), out_dtype, x)
     st = _lib.lib().nvfp4_gemv(
         x.data_ptr(), ldx, w_q.data_ptr(), w_s.data_ptr(), global_scale.data_ptr(), ids, T, share,
-        N, K, E, flags, out.data_ptr(), ldo, _raw_stream(stream, x))
+        N, K, E, flags, out.data_ptr(), ldo, _err_ptr(dev_err), _raw_stream(stream, x))
     _check(st, "nvfp4_gemv")
     return out
 

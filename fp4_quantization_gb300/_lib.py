@@ -40,7 +40,7 @@ SIGNATURES = {
     "mx_grouped_wgrad": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _u32,
                                         _vp, _vp, _vp]),
     "nvfp4_gemv": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64,
-                                  _u32, _vp, _i64, _vp]),
+                                  _u32, _vp, _i64, _vp, _vp]),
     "mxq_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_uint64, _vp, _vp]),
 }
 

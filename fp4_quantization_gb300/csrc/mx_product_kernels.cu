@@ -537,7 +537,8 @@ cudaError_t launch(const GroupedMaps& maps, const GroupedArgs& a, int num_sms,
   auto kernel = mx_grouped_kernel<CTAS, BN, WGRAD>;
   constexpr int smem = Shape<CTAS, BN>::SMEM;
   static_assert(smem <= 227 * 1024, "shared memory of one SM");
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), smem, &allowed);
   if (e != cudaSuccess) return e;
   // At most this many tiles, whatever the offsets are.
   constexpr int TILE_M = ROWS * CTAS;

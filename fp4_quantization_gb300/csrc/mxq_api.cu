@@ -66,6 +66,17 @@ mxq_status current_device(int* num_sms) {
   return MXQ_OK;
 }
 
+cudaError_t allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev % kMaxDevices);
+  if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // Encodes a tensor map of `rank` dimensions (innermost first) with no
 // swizzle; out-of-range loads read 0 and out-of-range stores are dropped.
 mxq_status encode_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,

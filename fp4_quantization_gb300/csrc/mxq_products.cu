@@ -140,12 +140,13 @@ mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, const uint8_
 mxq_status nvfp4_gemv(const void* x, int64_t ldx, const uint8_t* w_q, const uint8_t* w_s,
                       const float* w_global, const int32_t* experts, int64_t T, int64_t share,
                       int64_t N, int64_t K, int64_t E, uint32_t flags, void* out, int64_t ldo,
-                      mxq_stream_t stream) {
+                      uint32_t* dev_err, mxq_stream_t stream) {
   if (flags & ~static_cast<uint32_t>(MXQ_OUT_F32)) return MXQ_EINVAL;
   if (T < 0 || N < 0 || K < 0 || E < 0 || share < 1 || ldx < K || ldo < N) return MXQ_ESHAPE;
   if (!experts && (share != 1 || E != 1)) return MXQ_ESHAPE;
   if (K % 32) return MXQ_ESHAPE;
-  if (T > kMost || share > kMost || T * share > kMost || N > kMost || K > kMost || E > 65535)
+  if (T > kMost || share > kMost || T * share > kMost || N > kMost || K > kMost ||
+      E > mxq::GEMV_EXPERTS_MAX || E * (N / 16 + 1) > kMost)
     return MXQ_ESHAPE;
   int sms = 0;
   const mxq_status st = mxq::current_device(&sms);
@@ -174,6 +175,8 @@ mxq_status nvfp4_gemv(const void* x, int64_t ldx, const uint8_t* w_q, const uint
   a.out = out;
   a.ldo = ldo;
   a.out_f32 = size == 4;
+  a.dev_err = dev_err;
+  a.timeout_ns = mxq::PRODUCT_TIMEOUT_NS;
   return from_cuda(mxq::launch_nvfp4_gemv(a, sms, stream));
 }
 

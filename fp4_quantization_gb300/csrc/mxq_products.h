@@ -5,6 +5,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "mxq.h"
@@ -59,6 +60,8 @@ GroupedPlan grouped_plan(int64_t rows, int64_t cols, int64_t depth, int groups, 
 cudaError_t launch_grouped(const GroupedMaps& maps, const GroupedArgs& a, bool wgrad,
                            GroupedPlan plan, int num_sms, cudaStream_t stream);
 
+constexpr int GEMV_EXPERTS_MAX = 4096;
+
 struct GemvArgs {
   const uint16_t* x;        // bf16 [rows / share][ldx]
   int64_t ldx;
@@ -72,11 +75,17 @@ struct GemvArgs {
   void* out;
   int64_t ldo;
   int out_f32;
+  uint32_t* dev_err;
+  uint64_t timeout_ns;
 };
 
 cudaError_t launch_nvfp4_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream);
 
 // Host helpers (mxq_api.cu).
+// Allows `kernel` (a __global__ function) `bytes` of dynamic shared memory on the
+// current device; asks the runtime once for each device (*done holds a bit for
+// each), as the question takes longer than the rest of a launch's preparation.
+cudaError_t allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>* done);
 mxq_status current_device(int* num_sms);
 mxq_status encode_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
                       const cuuint64_t* dims, const cuuint64_t* strides_bytes,

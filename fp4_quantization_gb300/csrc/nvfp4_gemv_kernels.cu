@@ -23,8 +23,10 @@ namespace mxq {
 namespace {
 
 constexpr int WARPS = 8;
-constexpr int BLOCK_K = 256;   // K of one prefetch step of a warp: 2 x 16 bytes of codes a row
-constexpr int X_BYTES = 96 * 1024;   // staged rows of x: two CTAs share an SM
+constexpr int STEP_K = 256;          // K of one step of a warp: a line of codes a row
+constexpr int DEPTH = 4;             // steps of a warp in registers, three on their way
+constexpr int X_BYTES = 188 * 1024;  // staged rows of x
+constexpr int SUM_BYTES = 16 * 1024; // partial sums of some items
 
 __device__ __forceinline__ void store_out(const GemvArgs& a, int64_t row, int n, float v) {
   if (a.out_f32) {
@@ -67,323 +69,518 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The codes and scales that one thread multiplies in a step: of two rows, two
-// pieces of 32 values (16 bytes of codes, two block scales).
-struct Step {
-  uint4 c[2][2];
-  uint32_t s[2][2];
-};
-
-__device__ __forceinline__ void load_step(Step& w, const uint8_t* const (&q)[2],
-                                          const uint8_t* const (&s)[2], int k, int limit) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int at = k + 128 * j;
-      w.c[j][h] = make_uint4(0, 0, 0, 0);
-      w.s[j][h] = 0;
-      if (at < limit) {
-        w.c[j][h] = __ldg(reinterpret_cast<const uint4*>(q[h] + at / 2));
-        w.s[j][h] = __ldg(reinterpret_cast<const uint16_t*>(s[h] + at / 16));
-      }
-    }
-}
-
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// One step: x fragments from shared memory at xs, 4 pieces of [rows][4] 16-byte
-// units for each 128 of K.  Thread (g, t) holds weight rows g and g + 8, and
-// row g (and g + 8) of x, at the 32 values of k that its codes stand for; the
-// instruction's k order is the codes' order, on both sides.
-template <int TOKS>
-__device__ __forceinline__ void multiply_step(float (&acc)[TOKS / 8][4], const Step& w,
-                                              uint32_t xs, int rows, int g, int t) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    uint32_t sc[2][2];
+// What one thread holds of a step: of rows g and g + 8 the codes and the four
+// block scales of k = 64 t .. 64 t + 63.  A row's four threads read 128 bytes of
+// codes in one request.
+struct Step {
+  uint4 c[2][2];
+  uint32_t s[2];
+};
+
+__device__ __forceinline__ void load_32(uint4 (&v)[2], const uint8_t* p) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x),
+                 "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w) : "l"(p));
+}
+
+// Loads `left` values (what lies after them counts as 0) from rows q, s at this
+// thread's first.  aligned: rows of codes start on 32 bytes, of scales on 4.
+__device__ __forceinline__ void load_step(Step& w, const uint8_t* const (&q)[2],
+                                          const uint8_t* const (&s)[2], int left, bool aligned) {
+  if (aligned && left >= 64) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t s2 = e4m3x2_to_f16(w.s[j][h]);
-      sc[h][0] = prmt(s2, s2, 0x1010);
-      sc[h][1] = prmt(s2, s2, 0x3232);
+      load_32(w.c[h], q[h]);
+      w.s[h] = __ldg(reinterpret_cast<const uint32_t*>(s[h]));
+    }
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    w.s[h] = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w.c[h][i] = make_uint4(0, 0, 0, 0);
+      if (32 * i < left) {
+        w.c[h][i] = __ldg(reinterpret_cast<const uint4*>(q[h]) + i);
+        w.s[h] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(s[h]) + i))
+                  << (16 * i);
+      }
+    }
+  }
+}
+
+// One step: x fragments from shared memory at xs, 8 pieces of [rows][4] 16-byte
+// units.  Thread (g, t) multiplies weight rows g and g + 8, and row g (and g +
+// 8) of x, at the values of k that its codes stand for; the instruction's k
+// order is the codes' order, on both sides.
+template <int TOKS>
+__device__ __forceinline__ void multiply_step(float (&sum)[TOKS / 8][4], const Step& w,
+                                              uint32_t xs, int rows, int g, int t) {
+  float acc[2][TOKS / 8][4] = {};
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    uint32_t sc[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t pair = e4m3x2_to_f16(b < 2 ? w.s[h] & 0xFFFF : w.s[h] >> 16);
+      sc[h] = prmt(pair, pair, b % 2 ? 0x3232 : 0x1010);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int p = 2 * b; p < 2 * b + 2; ++p) {
       uint4 x[TOKS / 8];
 #pragma unroll
       for (int m = 0; m < TOKS / 8; ++m) {
         x[m] = make_uint4(0, 0, 0, 0);
-        if (g + 8 * m < rows)
-          x[m] = lds128(xs + (((j * 4 + i) * rows + g + 8 * m) * 4 + t) * 16);
+        if (g + 8 * m < rows) x[m] = lds128(xs + ((p * rows + g + 8 * m) * 4 + t) * 16);
       }
       uint32_t v[2][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        e2m1x8_to_f16(word(w.c[j][h], i), v[h]);
+        e2m1x8_to_f16(word(w.c[h][p / 4], p % 4), v[h]);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) v[h][p] = mul_f16x2(v[h][p], sc[h][i / 2]);
+        for (int n = 0; n < 4; ++n) v[h][n] = mul_f16x2(v[h][n], sc[h]);
       }
 #pragma unroll
       for (int m = 0; m < TOKS / 8; ++m) {
-        mma_f16(acc[m], v[0][0], v[1][0], v[0][1], v[1][1], x[m].x, x[m].y);
-        mma_f16(acc[m], v[0][2], v[1][2], v[0][3], v[1][3], x[m].z, x[m].w);
+        mma_f16(acc[0][m], v[0][0], v[1][0], v[0][1], v[1][1], x[m].x, x[m].y);
+        mma_f16(acc[1][m], v[0][2], v[1][2], v[0][3], v[1][3], x[m].z, x[m].w);
       }
     }
   }
+  // Sums of 128 terms at a time: the instruction cuts its sums off.
+#pragma unroll
+  for (int m = 0; m < TOKS / 8; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[m][i] += acc[0][m][i] + acc[1][m][i];
 }
 
-// A CTA multiplies 16 * tiles weight rows by up to TOKS rows of x over its part
-// of K; its 8 warps are `tiles` row tiles x 8 / tiles parts of K (taken step
-// by step in turn).  The parts' sums are added through shared memory, and
-// those of a cluster's CTAs through the first one's, in a fixed order.
+// Persistent CTAs (clusters of them) take an equal share each of the items
+// (an expert that has rows, 16 * tiles of its output columns) in order, so
+// that a CTA stages its rows of x once for many items.  A CTA's 8 warps are
+// `tiles` tiles of 16 columns x 8 / tiles parts of K (taken step by step in
+// turn); a cluster's CTAs split K into ranges.  The parts leave their sums in
+// shared memory; when its places are full, or the rows of x change, they are
+// added in a fixed order, and those of a cluster's CTAs by its first one.
 template <int TOKS>
-__global__ void __launch_bounds__(32 * WARPS, 2)
-nvfp4_gemv_kernel(const GemvArgs a, const int tiles, const int cluster, const int by_row) {
+__global__ void __launch_bounds__(32 * WARPS, 1)
+nvfp4_gemv_kernel(const GemvArgs a, const int tiles, const int cluster) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_up_shared<16>(smem_raw);
-  float* red = reinterpret_cast<float*>(smem);            // [warp][16][TOKS]
-  const uint32_t xs = smem_addr(smem + WARPS * 16 * TOKS * 4);
-  __shared__ int list[TOKS];
-  __shared__ int found, next_row;
+  float* red = reinterpret_cast<float*>(smem);            // [item][warp][row][16]
+  const uint32_t xs = smem_addr(smem + SUM_BYTES);
+  __shared__ uint32_t present[GEMV_EXPERTS_MAX / 32];
+  __shared__ uint16_t active[GEMV_EXPERTS_MAX];           // the experts that have rows
+  __shared__ int warp_sum[WARPS];
+  __shared__ int list[TOKS + 2];                          // rows of the expert, their number, the next
+  __shared__ int best_of[TOKS / 8 * WARPS];
   __shared__ int top[TOKS];                               // largest magnitude left of each row
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
-  const int rank = blockIdx.x % cluster, n0 = blockIdx.x / cluster * tiles * 16;
-  const int cols = min(tiles * 16, a.n - n0);
+  const int rank = blockIdx.x % cluster;
+  const int groups = (a.n + tiles * 16 - 1) / (tiles * 16);
 
-  // This CTA's expert.  by_row: the one of row blockIdx.y, unless an earlier
-  // row has it already.
-  int e = blockIdx.y, from = 0;
-  if (by_row) {
-    from = blockIdx.y;
-    e = a.experts[from];
-    bool mine = true;
-    for (int i = tid; i < from; i += 32 * WARPS) mine &= a.experts[i] != e;
-    if (e < 0 || e >= a.num_experts) {
-      for (int i = tid; rank == 0 && i < cols; i += 32 * WARPS) store_out(a, from, n0 + i, 0.f);
+  // Which experts have rows; rows without an expert are zero.
+  int experts = 1;
+  if (a.experts) {
+    const int words = (a.num_experts + 31) / 32;
+    static_assert(GEMV_EXPERTS_MAX / 32 <= 32 * WARPS, "a word a thread");
+    if (tid < words) present[tid] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int r0 = warp * 32; r0 < a.rows; r0 += 32 * WARPS) {
+      const int id = r0 + lane < a.rows ? a.experts[r0 + lane] : 0;
+      const bool none = id < 0 || id >= a.num_experts;
+      if (r0 + lane < a.rows && !none) atomicOr(&present[id / 32], 1u << (id % 32));
+      for (uint32_t m = __ballot_sync(~0u, none); m; m &= m - 1)
+        for (int n = blockIdx.x * 32 + lane; n < a.n; n += gridDim.x * 32)
+          store_out(a, r0 + __ffs(m) - 1, n, 0.f);
+    }
+    __syncthreads();
+    const uint32_t mine = tid < words ? present[tid] : 0;
+    int sum = __popc(mine);
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int up = __shfl_up_sync(~0u, sum, d);
+      if (lane >= d) sum += up;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    int at = sum - __popc(mine);
+    experts = 0;
+#pragma unroll 1
+    for (int i = 0; i < (words + 31) / 32; ++i) {
+      if (i < warp) at += warp_sum[i];
+      experts += warp_sum[i];
+    }
+    for (uint32_t m = mine; m; m &= m - 1)
+      active[at++] = static_cast<uint16_t>(tid * 32 + __ffs(m) - 1);
+    __syncthreads();
+  }
+  const int items = experts * groups;
+  const int clusters = gridDim.x / cluster, me = blockIdx.x / cluster;
+  const int each = items / clusters, extra = items % clusters;
+  const int item_first = me * each + min(me, extra), item_end = item_first + each + (me < extra);
+  if (item_first == item_end) return;
+
+  // This CTA's range of K, and this warp's steps in it.
+  const int parts = WARPS / tiles, tile = warp % tiles, part = warp / tiles;
+  const int steps = (a.k + STEP_K - 1) / STEP_K, range = (steps + cluster - 1) / cluster;
+  const int k_first = min(rank * range, steps) * STEP_K;
+  const int k_end = min(min((rank + 1) * range, steps) * STEP_K, a.k);
+  struct Item {
+    int e, n0;            // its expert and first output column
+  };
+  auto item_at = [&](int i) {
+    const int nth = a.experts ? i / groups : 0;
+    return Item{a.experts ? static_cast<int>(active[nth]) : 0, (i - nth * groups) * tiles * 16};
+  };
+  // K is staged in chunks of `room` at most (one, unless rows and K are both
+  // large); a warp's steps in the chunk from k0 on start at start_of(k0).
+  constexpr int room = X_BYTES / (TOKS * 2) / STEP_K * STEP_K;
+  const int turn = parts * STEP_K;
+  auto start_of = [&](int k0) {
+    const int behind = (k0 - k_first - part * STEP_K) % turn;
+    return behind <= 0 ? k0 - behind : k0 + turn - behind;
+  };
+  // This warp's loads: DEPTH steps (or places for them) at a time, in order over
+  // the chunks and the items.
+  const bool aligned = a.k % 64 == 0 && (reinterpret_cast<uintptr_t>(a.w_q) & 31) == 0;
+  const uint8_t *q[2] = {}, *s[2] = {};               // this thread's codes and scales at k = 0
+  int load_item = item_first, load_k0 = k_first, load_k = 0;
+  auto load_start = [&] {
+    load_k = start_of(load_k0);
+    if (load_item >= item_end) return;
+    const Item item = item_at(load_item);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t n = static_cast<int64_t>(item.e) * a.n +
+                        min(item.n0 + tile * 16 + g + 8 * h, a.n - 1);
+      q[h] = a.w_q + n * (a.k / 2) + 32 * t;
+      s[h] = a.w_s + n * (a.k / 16) + 4 * t;
+    }
+  };
+  auto load_next = [&](Step& w, bool last) {          // last of DEPTH
+    const int k1 = min(load_k0 + room, k_end);
+    if (load_item < item_end && load_k < k1) {
+      const uint8_t* const qk[2] = {q[0] + load_k / 2, q[1] + load_k / 2};
+      const uint8_t* const sk[2] = {s[0] + load_k / 16, s[1] + load_k / 16};
+      load_step(w, qk, sk, a.k - load_k - 64 * t, aligned);
+    }
+    load_k += turn;
+    if (last && load_k >= k1) {
+      load_k0 += room;
+      if (load_k0 >= k_end) {
+        load_k0 = k_first;
+        ++load_item;
+      }
+      load_start();
+    }
+  };
+  Step w[DEPTH] = {};
+  int held_item = -1, held_k0 = 0;                    // the chunk that they hold the start of
+
+  // Up to TOKS rows of expert e from row `from` on: `found` of them, row_at(i);
+  // next_row is then the next one after them.
+  int found = 0, next_row = 0, row0 = 0;
+  auto list_rows = [&](int e, int from) {
+    if (!a.experts) {
+      row0 = from;
+      found = min(TOKS, a.rows - from);
+      next_row = from + found;
       return;
     }
-    if (!__syncthreads_and(mine)) return;
-  } else if (a.experts && blockIdx.y == 0 && rank == 0) {
-    for (int r = 0; r < a.rows; ++r) {
-      const int id = a.experts[r];
-      if (id < 0 || id >= a.num_experts)
-        for (int i = tid; i < cols; i += 32 * WARPS) store_out(a, r, n0 + i, 0.f);
-    }
-  }
-
-  // This warp's weight rows and steps.
-  const int parts = WARPS / tiles, tile = warp % tiles, part = warp / tiles;
-  const uint8_t *q[2], *s[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t n = static_cast<int64_t>(e) * a.n + min(n0 + tile * 16 + g + 8 * h, a.n - 1);
-    q[h] = a.w_q + n * (a.k / 2);
-    s[h] = a.w_s + n * (a.k / 16);
-  }
-  const int steps = (a.k + BLOCK_K - 1) / BLOCK_K, share = (steps + cluster - 1) / cluster;
-  const int k_first = min(rank * share, steps) * BLOCK_K;
-  const int k_end = min(min((rank + 1) * share, steps) * BLOCK_K, a.k);
-  int exp_g;
-  const float frac_g = frexpf(a.w_global[e], &exp_g);
-  Step w;
-  load_step(w, q, s, k_first + part * BLOCK_K + 32 * t, k_end);   // before x is known
-
-  if (tid == 0) next_row = from;
-  __syncthreads();
-  while (next_row < a.rows) {
-    // Up to TOKS rows of this expert.
     __syncthreads();
     if (warp == 0) {
-      int at = next_row, have = 0;
-      while (at < a.rows && have < TOKS) {
+      int at = from, have = 0;
+      bool past = false;
+      while (at < a.rows && !past) {
         const int r = at + lane;
-        const bool hit = r < a.rows && (!a.experts || a.experts[r] == e);
-        const uint32_t hits = __ballot_sync(~0u, hit);
-        const int place = have + __popc(hits & ((1u << lane) - 1));
-        if (hit && place < TOKS) list[place] = r;
-        const int room = TOKS - have;
-        if (__popc(hits) > room) {      // the row after the last one taken
-          at += __fns(hits, 0, room + 1);
-          have = TOKS;
-        } else {
-          at += 32;
-          have += __popc(hits);
-        }
+        const uint32_t hits = __ballot_sync(~0u, r < a.rows && a.experts[r] == e);
+        const int place = have + __popc(hits & ((1u << lane) - 1)), room = TOKS - have;
+        if ((hits >> lane & 1) && place < TOKS) list[place] = r;
+        past = __popc(hits) > room;
+        at += past ? static_cast<int>(__fns(hits, 0, room + 1)) : 32;
+        have = min(have + __popc(hits), TOKS);
       }
       if (lane == 0) {
-        found = have;
-        next_row = at;
+        list[TOKS] = have;
+        list[TOKS + 1] = at;
       }
     }
     __syncthreads();
-    const int rows = found;
-    if (rows == 0) break;
+    found = list[TOKS];
+    next_row = list[TOKS + 1];
+  };
+  auto row_at = [&](int m) { return a.experts ? list[m] : row0 + m; };
 
-    float out[TOKS / 8][4] = {};
-    const int room_k = X_BYTES / (rows * 2) / BLOCK_K * BLOCK_K;
-    for (int k0 = k_first; k0 < k_end; k0 += room_k) {
-      const int k1 = min(k0 + room_k, k_end);
-      const int pieces = (k1 - k0) / 8;          // 16-byte pieces of a row of x
-      const int per = rows <= 1 ? 8 : rows <= 2 ? 4 : rows <= 4 ? 2 : 1;   // warps a row
-      int below = 256;                           // exponents still to take (this warp's rows)
-      int below2 = 256;
-      bool more = true;
-      while (more) {
-        if (tid < TOKS) top[tid] = 0;
-        __syncthreads();
-        for (int m = warp / per; m < rows; m += WARPS / per) {
-          const uint16_t* x = a.x + static_cast<int64_t>(list[m] / a.share) * a.ldx + k0;
-          const uint32_t lim = (m < WARPS / per ? below : below2) << 7;
-          uint32_t best = 0;
-          for (int p = (warp % per) * 32 + lane; p < pieces; p += per * 32) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(x) + p);
+  bool again = false;           // something is staged
+  // Stages rows [0, rows) of the list from k0 to k1, each piece of 8 values
+  // where the multiplication reads it: first as they are, then, when the rows'
+  // largest magnitudes below `below` are known, the window from there down as
+  // f16.  True where smaller ones are left.
+  auto stage = [&](int rows, int k0, int k1, int (&below)[TOKS / 8]) {
+    const int all = (k1 - k0 + STEP_K - 1) / STEP_K * (STEP_K / 8);
+    const int per = rows <= 1 ? 8 : rows <= 2 ? 4 : rows <= 4 ? 2 : 1;   // warps a row
+    const int p0 = (warp % per) * 32 + lane;
+    // Piece p is k = 8 p: of its 256, thread (p / 8) % 4's piece p % 8.
+    auto place = [&](int m, int p) {
+      return xs + (((p / 32 * 8 + p % 8) * rows + m) * 4 + p / 8 % 4) * 16;
+    };
+    if (again) __syncthreads();            // the last reads of what was staged before
+    again = true;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t lo = word(v, i) & 0x7FFF, hi = (word(v, i) >> 16) & 0x7FFF;
-              if (lo < lim) best = max(best, lo);
-              if (hi < lim) best = max(best, hi);
-            }
-          }
-          best = __reduce_max_sync(~0u, best);
-          if (lane == 0) atomicMax(&top[m], static_cast<int>(best));
-        }
-        __syncthreads();
-        bool left = false;
-        for (int m = warp / per; m < rows; m += WARPS / per) {
-          const uint16_t* x = a.x + static_cast<int64_t>(list[m] / a.share) * a.ldx + k0;
-          int& mine = m < WARPS / per ? below : below2;
-          const uint32_t lim = mine << 7;
-          const int high = top[m] >> 7;
-          const uint32_t low = max(high - 28, 0) << 7;
-          const float up = __uint_as_float(static_cast<uint32_t>(min(141 - high, 127) + 127) << 23);
-          for (int p = (warp % per) * 32 + lane; p < (k1 - k0 + BLOCK_K - 1) / BLOCK_K * (BLOCK_K / 8);
-               p += per * 32) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (p < pieces) v = __ldg(reinterpret_cast<const uint4*>(x) + p);
-            uint32_t o[4];
+    for (int i = 0; i < TOKS / 8; ++i) {
+      const int m = warp / per + i * WARPS;
+      if (m >= rows) break;
+      const uint32_t lim = below[i] << 7;
+      const int row = row_at(m);
+      const uint4* x = reinterpret_cast<const uint4*>(
+          a.x + static_cast<int64_t>(a.share == 1 ? row : row / a.share) * a.ldx + k0);
+      uint32_t best = 0;
+#pragma unroll 4
+      for (int p = p0; p < all; p += per * 32) {
+        const uint4 v = 8 * p < k1 - k0 ? __ldg(x + p) : make_uint4(0, 0, 0, 0);
+        sts128(place(m, p), v.x, v.y, v.z, v.w);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t lo = word(v, i) & 0x7FFF, hi = (word(v, i) >> 16) & 0x7FFF;
-              left |= (lo < low && lo != 0) || (hi < low && hi != 0);
-              const float f0 = lo >= low && lo < lim ? bf16_lo(word(v, i)) * up : 0.f;
-              const float f1 = hi >= low && hi < lim ? bf16_hi(word(v, i)) * up : 0.f;
-              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(f1), "f"(f0));
-            }
-            // Piece p is k = 8 p: of its 128, thread t = (p / 4) % 4's piece p % 4.
-            sts128(xs + (((p / 16 * 4 + p % 4) * rows + m) * 4 + p / 4 % 4) * 16, o[0], o[1], o[2],
-                   o[3]);
-          }
-          mine = max(high - 28, 0);
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t lo = word(v, j) & 0x7FFF, hi = (word(v, j) >> 16) & 0x7FFF;
+          if (lo < lim) best = max(best, lo);
+          if (hi < lim) best = max(best, hi);
         }
-        more = __syncthreads_or(left);
+      }
+      best = __reduce_max_sync(~0u, best);
+      if (lane == 0) best_of[i * WARPS + warp] = static_cast<int>(best);
+    }
+    __syncthreads();
+    bool left = false;
+#pragma unroll
+    for (int i = 0; i < TOKS / 8; ++i) {
+      const int m = warp / per + i * WARPS;
+      if (m >= rows) break;
+      const uint32_t lim = below[i] << 7;
+      int most = lane < per ? best_of[i * WARPS + warp / per * per + lane] : 0;
+      most = __reduce_max_sync(~0u, most);
+      if (lane == 0) top[m] = most;        // the same from each of the row's warps
+      const int high = most >> 7;
+      const uint32_t low = max(high - 28, 0) << 7;
+      const float up = __uint_as_float(static_cast<uint32_t>(min(141 - high, 127) + 127) << 23);
+#pragma unroll 1
+      for (int p = p0; p < all; p += per * 32) {
+        const uint4 v = lds128(place(m, p));
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t lo = word(v, j) & 0x7FFF, hi = (word(v, j) >> 16) & 0x7FFF;
+          left |= (lo < low && lo != 0) || (hi < low && hi != 0);
+          const float f0 = lo >= low && lo < lim ? bf16_lo(word(v, j)) * up : 0.f;
+          const float f1 = hi >= low && hi < lim ? bf16_hi(word(v, j)) * up : 0.f;
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(f1), "f"(f0));
+        }
+        sts128(place(m, p), o[0], o[1], o[2], o[3]);
+      }
+      below[i] = max(high - 28, 0);
+    }
+    return __syncthreads_or(left) != 0;
+  };
 
-        float sum[TOKS / 8][4] = {};
-        for (int k = k0 + part * BLOCK_K; k < k1; k += parts * BLOCK_K) {
-          Step now = w;
-          int ahead = k + parts * BLOCK_K;
-          if (ahead >= k1) ahead = (more ? k0 : k1) + part * BLOCK_K;
-          load_step(w, q, s, ahead + 32 * t, k_end);
-          // Sums of 256 terms at a time: the instruction cuts its sums off.
-          float acc[TOKS / 8][4] = {};
-          multiply_step<TOKS>(acc, now, xs + (k - k0) * rows * 2, rows, g, t);
+  // Adds the sums of `count` items from the first one on and writes them: a
+  // thread a column, a pair of an item and a row at a time.
+  auto flush = [&](int first, int count, int rows) {
+    const int width = tiles * 16, col = tid % width, step = 32 * WARPS / width;
+    __syncthreads();
+    auto place = [&](int pair, int p) {
+      const int n = rows == 1 ? pair : pair / rows, r = pair - n * rows;
+      return red + ((n * WARPS + p * tiles + col / 16) * rows + r) * 16 + col % 16;
+    };
+    auto write = [&](int pair, float v) {
+      const int n = rows == 1 ? pair : pair / rows, at = item_at(first + n).n0 + col;
+      if (at < a.n) store_out(a, row_at(pair - n * rows), at, v);
+    };
+#pragma unroll 1
+    for (int pair = tid / width; pair < count * rows; pair += step) {
+      float v = 0;
+#pragma unroll 1
+      for (int p = 0; p < parts; ++p) v += *place(pair, p);
+      if (cluster == 1) write(pair, v);
+      else *place(pair, 0) = v;             // this thread's own
+    }
+    if (cluster == 1) {
+      __syncthreads();
+      return;
+    }
+    cluster_sync();
+#pragma unroll 1
+    for (int pair = tid / width * cluster + rank; pair < count * rows; pair += step * cluster) {
+      const uint32_t at = smem_addr(place(pair, 0));
+      float v = 0;
+#pragma unroll
+      for (int p = 0; p < 8; ++p)
+        if (p < cluster) v += ld_cluster_f32(at, p);
+      write(pair, v);
+    }
+    cluster_sync();
+  };
+
+  int cur = -1;                 // the expert whose rows are listed,
+  bool whole = false;           // all of them,
+  int staged = -1;              // and which start of K is staged (in one window)
+  int first = item_first;       // the first item whose sums wait
+  for (int item = item_first; item < item_end; ++item) {
+    const Item here = item_at(item);
+    if (here.e != cur || !whole) {
+      if (item > first) flush(first, item - first, found);
+      first = item;
+      list_rows(here.e, 0);
+      cur = here.e;
+      whole = next_row >= a.rows;
+      staged = -1;
+    }
+    const float global = a.w_global[here.e];
+    while (true) {
+      const int rows = found, after = next_row;
+      float out[TOKS / 8][4] = {};
+      for (int k0 = k_first; k0 < k_end; k0 += room) {
+        const int k1 = min(k0 + room, k_end);
+        int below[TOKS / 8];                       // exponents still to take (this warp's rows)
+#pragma unroll
+        for (int i = 0; i < TOKS / 8; ++i) below[i] = 256;
+        bool more = staged != k0;
+        for (int window = 0; window == 0 || more; ++window) {
+          if (more) {
+            more = stage(rows, k0, k1, below);
+            staged = window == 0 && !more ? k0 : -1;
+          }
+          float sum[TOKS / 8][4] = {};
+          // DEPTH steps at a time: each is multiplied and its place loaded again.
+          // Where the places hold something else, the first round only loads.
+          bool fill = item != held_item || k0 != held_k0;
+          if (fill) {
+            load_item = item;
+            load_k0 = k0;
+            load_start();
+          }
+          int k = start_of(k0);
+          bool filled = false;
+          do {
+            filled = fill;
+#pragma unroll
+            for (int i = 0; i < DEPTH; ++i) {
+              if (!fill && k < k1)
+                multiply_step<TOKS>(sum, w[i], xs + (k - k0) * rows * 2, rows, g, t);
+              load_next(w[i], i == DEPTH - 1);
+              if (!fill) k += turn;
+            }
+            fill = false;
+          } while (filled || k < k1);
+          held_item = k0 + room < k_end ? item : item + 1;     // what the loads have begun
+          held_k0 = k0 + room < k_end ? k0 + room : k_first;
+          int exp_g;
+          const float frac_g = frexpf(global, &exp_g);
+          // To the output's units; both scales in one step, so that only a
+          // result out of fp32's range leaves it.
 #pragma unroll
           for (int m = 0; m < TOKS / 8; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum[m][i] += acc[m][i];
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * m + 2 * t + i % 2;
+              const int high = r < rows ? top[r] >> 7 : 0;
+              out[m][i] += ldexpf(sum[m][i] * frac_g, exp_g - min(141 - high, 127));
+            }
         }
-        // To the output's units; both scales in one step, so that only a
-        // result out of fp32's range leaves it.
-#pragma unroll
-        for (int m = 0; m < TOKS / 8; ++m)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 8 * m + 2 * t + i % 2;
-            const int high = r < rows ? top[r] >> 7 : 0;
-            out[m][i] += ldexpf(sum[m][i] * frac_g, exp_g - min(141 - high, 127));
-          }
-        __syncthreads();
       }
-    }
-
-    // Sums of this CTA's parts of K, then of the cluster's.
 #pragma unroll
-    for (int m = 0; m < TOKS / 8; ++m)
+      for (int m = 0; m < TOKS / 8; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        red[(warp * TOKS + 8 * m + 2 * t + i % 2) * 16 + g + 8 * (i / 2)] = out[m][i];
-    __syncthreads();
-    for (int i = tid; i < tiles * 16 * rows; i += 32 * WARPS) {
-      const int col = i % (tiles * 16), r = i / (tiles * 16);
-      float v = 0;
-      for (int p = 0; p < parts; ++p)
-        v += red[((p * tiles + col / 16) * TOKS + r) * 16 + col % 16];
-      if (cluster == 1) {
-        if (col < cols) store_out(a, list[r], n0 + col, v);
-      } else {
-        red[((col / 16) * TOKS + r) * 16 + col % 16] = v;   // part 0's place, this thread's own
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * m + 2 * t + i % 2;
+          if (r < rows)
+            red[(((item - first) * WARPS + warp) * rows + r) * 16 + g + 8 * (i / 2)] = out[m][i];
+        }
+      const int room = SUM_BYTES / (WARPS * 16 * 4) / rows;      // items
+      if (after < a.rows || item + 1 - first == room || item + 1 == item_end) {
+        flush(first, item + 1 - first, rows);
+        first = item + 1;
       }
+      if (after >= a.rows) break;
+      // More rows than one pass takes: the weights again.
+      list_rows(here.e, after);
+      first = item;
+      staged = -1;
     }
-    if (cluster > 1) {
-      cluster_sync();
-      for (int i = tid; rank == 0 && i < cols * rows; i += 32 * WARPS) {
-        const int col = i % cols, r = i / cols;
-        const uint32_t at = smem_addr(red + ((col / 16) * TOKS + r) * 16 + col % 16);
-        float v = 0;
-        for (int p = 0; p < cluster; ++p) v += ld_cluster_f32(at, p);
-        store_out(a, list[r], n0 + col, v);
-      }
-      cluster_sync();
-    }
-    // More rows than one pass takes: the weights again from the start.
-    if (next_row < a.rows) load_step(w, q, s, k_first + part * BLOCK_K + 32 * t, k_end);
-    __syncthreads();
   }
 }
 
+// How the work is cut: 16 * tiles output columns a CTA, K over clusters.
+struct Plan {
+  int tiles, cluster;
+};
+
+// The plan with the least estimated time: a round of steps (256 x 16 weights
+// for each warp of the GPU) takes 0.45 us, a cluster's barriers 1 us for each
+// time that sums are added, and staging x 2 us and 0.02 us a thousand values.
+Plan choose(const GemvArgs& a, int rows, int64_t slots, int num_sms) {
+  const int64_t steps = (a.k + STEP_K - 1) / STEP_K;
+  Plan best{1, 1};
+  double least = 1e30;
+  for (int cluster = 1; cluster <= 8; cluster *= 2) {
+    if (cluster > 1 && steps < cluster) break;
+    const int64_t range = (steps + cluster - 1) / cluster;
+    const double staging = 2 + 2e-5 * rows * range * STEP_K;
+    const bool fits = rows * range * STEP_K * 2 <= X_BYTES;
+    for (int tiles = 1; tiles <= WARPS; tiles *= 2) {
+      const int parts = WARPS / tiles;
+      const int64_t items = (a.n + tiles * 16 - 1) / (tiles * 16) * slots;
+      const int64_t at_once = num_sms / cluster;
+      const double turns = static_cast<double>((items + at_once - 1) / at_once);
+      const double item = 0.45 * ((range + parts - 1) / parts) + (cluster > 1 ? 1.0 : 0) + 0.1;
+      const double time = turns * (item + (fits ? 0 : staging)) + staging;
+      if (time < least) {
+        least = time;
+        best = {tiles, cluster};
+      }
+    }
+  }
+  return best;
+}
+
 template <int TOKS>
-cudaError_t launch(const GemvArgs& a, int tiles, int cluster, int slots, bool by_row,
+cudaError_t launch(const GemvArgs& a, Plan plan, int64_t slots, int num_sms,
                    cudaStream_t stream) {
-  constexpr int smem = X_BYTES + WARPS * 16 * TOKS * 4 + 16;
-  cudaError_t e = cudaFuncSetAttribute(nvfp4_gemv_kernel<TOKS>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int smem = X_BYTES + SUM_BYTES + 16;
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e =
+      allow_shared(reinterpret_cast<const void*>(nvfp4_gemv_kernel<TOKS>), smem, &allowed);
   if (e != cudaSuccess) return e;
-  const int groups = (a.n + tiles * 16 - 1) / (tiles * 16);
+  const int64_t items = (a.n + plan.tiles * 16 - 1) / (plan.tiles * 16) * slots;
+  const int64_t most = num_sms / plan.cluster;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(groups) * cluster, slots);
+  cfg.gridDim = dim3(static_cast<unsigned>(items < most ? items : most) * plan.cluster);
   cfg.blockDim = dim3(32 * WARPS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.x = plan.cluster;
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, nvfp4_gemv_kernel<TOKS>, a, tiles, cluster, by_row ? 1 : 0);
+  return cudaLaunchKernelEx(&cfg, nvfp4_gemv_kernel<TOKS>, a, plan.tiles, plan.cluster);
 }
 
 }  // namespace
 
 cudaError_t launch_nvfp4_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream) {
-  // A grid row for each expert, or for each row where there are fewer rows.
-  const bool by_row = a.experts && a.rows <= a.num_experts && a.rows <= 65535;
-  const int slots = !a.experts ? 1 : by_row ? a.rows : a.num_experts;
-  // Rows that a CTA is likely to multiply at once.
-  const int rows = a.experts ? (a.rows + a.num_experts - 1) / a.num_experts : a.rows;
-  const int steps = (a.k + BLOCK_K - 1) / BLOCK_K;
-  // Enough CTAs for two on every SM, with the fewest parts of K.
-  const int64_t row_tiles = (static_cast<int64_t>(a.n) + 15) / 16;
-  int tiles = 8, cluster = 1;
-  while (tiles > 1 && (row_tiles + tiles - 1) / tiles * slots < 2 * num_sms) tiles /= 2;
-  while (cluster < 8 && (row_tiles + tiles - 1) / tiles * slots * cluster < num_sms &&
-         steps > 2 * cluster * (WARPS / tiles))
-    cluster *= 2;
-  return rows > 8 ? launch<16>(a, tiles, cluster, slots, by_row, stream)
-                  : launch<8>(a, tiles, cluster, slots, by_row, stream);
+  // At most this many experts have rows, and then this many rows each.
+  const int64_t slots = !a.experts ? 1 : a.rows < a.num_experts ? a.rows : a.num_experts;
+  const int rows = a.experts ? static_cast<int>((a.rows + slots - 1) / slots) : a.rows;
+  const Plan plan = choose(a, rows < 16 ? rows : 16, slots, num_sms);
+  return rows > 8 ? launch<16>(a, plan, slots, num_sms, stream)
+                  : launch<8>(a, plan, slots, num_sms, stream);
 }
 
 }  // namespace mxq

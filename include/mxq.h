@@ -379,7 +379,8 @@ MXQ_API mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, cons
  *
  *   x       [T][ldx] bf16, ldx % 8 == 0; K % 32 == 0; N is any.
  *   share   output rows that read one row of x (a token's experts), >= 1.
- *   w_q [E][N][K/2], w_s [E][N][K/16], w_global [E] fp32 on the device.
+ *   w_q [E][N][K/2], w_s [E][N][K/16], w_global [E] fp32 on the device;
+ *           E <= 4096.
  *   experts [T * share] int32 on the device: a row whose expert is negative
  *           or >= E is zero (it belongs to another rank, or to no token).
  *           NULL: one weight (E == 1, share == 1).
@@ -390,7 +391,7 @@ MXQ_API mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, cons
 MXQ_API mxq_status nvfp4_gemv(const void* x, int64_t ldx, const uint8_t* w_q, const uint8_t* w_s,
                               const float* w_global, const int32_t* experts, int64_t T,
                               int64_t share, int64_t N, int64_t K, int64_t E, uint32_t flags,
-                              void* out, int64_t ldo, mxq_stream_t stream);
+                              void* out, int64_t ldo, uint32_t* dev_err, mxq_stream_t stream);
 
 /*
  * mxq_selftest_bounded_wait -- launches one warp that waits on a barrier

@@ -454,7 +454,7 @@ def test_gemv_refusals():
     L = _lib.lib()
 
     def gemv(ldx=64, T=1, share=1, N=64, K=64, E=1, flags=0, ldo=64, experts=P):
-        return L.nvfp4_gemv(P, ldx, P, P, P, experts, T, share, N, K, E, flags, P, ldo, None)
+        return L.nvfp4_gemv(P, ldx, P, P, P, experts, T, share, N, K, E, flags, P, ldo, None, None)
 
     assert gemv(flags=16) == 1
     for bad in (dict(T=-1), dict(share=0), dict(N=-1), dict(K=40), dict(ldx=32), dict(ldo=63),
@@ -475,8 +475,8 @@ def test_device_refusals():
     assert L.mx_grouped_gemm(b, b, b, b, b, 64, 64, 64, 2, 0, b + 1, 64, None, None) == 3
     assert L.mx_grouped_wgrad(b, b, b, b, b, 64, 64, 64, 2, 0, None, None, None) == 1
     assert L.mx_grouped_wgrad(b, b, b, b + 4, b, 64, 64, 64, 2, 0, b, None, None) == 3
-    assert L.nvfp4_gemv(None, 64, b, b, b, None, 1, 1, 64, 64, 1, 0, b, 64, None) == 1
-    assert L.nvfp4_gemv(b, 60, b, b, b, None, 1, 1, 64, 32, 1, 0, b, 64, None) == 3
+    assert L.nvfp4_gemv(None, 64, b, b, b, None, 1, 1, 64, 64, 1, 0, b, 64, None, None) == 1
+    assert L.nvfp4_gemv(b, 60, b, b, b, None, 1, 1, 64, 32, 1, 0, b, 64, None, None) == 3
     gen = generator(14)
     q, s = mx_operand(gen, True, 32, 64)
     w, ws = mx_operand(gen, True, 2, 32, 64)
