@@ -146,7 +146,7 @@ mxq_status nvfp4_gemv(const void* x, int64_t ldx, const uint8_t* w_q, const uint
   if (!experts && (share != 1 || E != 1)) return MXQ_ESHAPE;
   if (K % 32) return MXQ_ESHAPE;
   if (T > kMost || share > kMost || T * share > kMost || N > kMost || K > kMost ||
-      E > mxq::GEMV_EXPERTS_MAX || E * (N / 16 + 1) > kMost)
+      E > mxq::GEMV_EXPERTS_MAX || E * (N + 16) > kMost)
     return MXQ_ESHAPE;
   int sms = 0;
   const mxq_status st = mxq::current_device(&sms);

@@ -24,9 +24,18 @@ namespace {
 
 constexpr int WARPS = 8;
 constexpr int STEP_K = 256;          // K of one step of a warp: a line of codes a row
-constexpr int DEPTH = 4;             // steps of a warp in registers, three on their way
-constexpr int X_BYTES = 188 * 1024;  // staged rows of x
-constexpr int SUM_BYTES = 16 * 1024; // partial sums of some items
+constexpr int STEP_BYTES = 16 * STEP_K / 2;
+constexpr int SUM_BYTES = 8 * 1024;  // partial sums of some items
+
+// Rows of x at a time: up to 8 or 16.  Two CTAs share an SM.
+template <int TOKS>
+struct Shape {
+  static constexpr int TILES = TOKS / 8;                 // of 8 columns of the instruction
+  static constexpr int DEPTH = TOKS == 16 ? 3 : 4;       // steps of a warp in shared memory
+  static constexpr int RING_BYTES = WARPS * DEPTH * STEP_BYTES;
+  static constexpr int X_BYTES = (TOKS == 16 ? 44 : 28) * 1024;   // staged rows of x
+  static constexpr int SMEM = RING_BYTES + X_BYTES + SUM_BYTES + 1024;
+};
 
 __device__ __forceinline__ void store_out(const GemvArgs& a, int64_t row, int n, float v) {
   if (a.out_f32) {
@@ -73,80 +82,50 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// What one thread holds of a step: of rows g and g + 8 the codes and the four
-// block scales of k = 64 t .. 64 t + 63.  A row's four threads read 128 bytes of
-// codes in one request.
-struct Step {
-  uint4 c[2][2];
-  uint32_t s[2];
-};
-
-__device__ __forceinline__ void load_32(uint4 (&v)[2], const uint8_t* p) {
-  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x),
-                 "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w) : "l"(p));
-}
-
-// Loads `left` values (what lies after them counts as 0) from rows q, s at this
-// thread's first.  aligned: rows of codes start on 32 bytes, of scales on 4.
-__device__ __forceinline__ void load_step(Step& w, const uint8_t* const (&q)[2],
-                                          const uint8_t* const (&s)[2], int left, bool aligned) {
-  if (aligned && left >= 64) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      load_32(w.c[h], q[h]);
-      w.s[h] = __ldg(reinterpret_cast<const uint32_t*>(s[h]));
-    }
-    return;
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    w.s[h] = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      w.c[h][i] = make_uint4(0, 0, 0, 0);
-      if (32 * i < left) {
-        w.c[h][i] = __ldg(reinterpret_cast<const uint4*>(q[h]) + i);
-        w.s[h] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(s[h]) + i))
-                  << (16 * i);
-      }
-    }
-  }
-}
-
-// One step: x fragments from shared memory at xs, 8 pieces of [rows][4] 16-byte
-// units.  Thread (g, t) multiplies weight rows g and g + 8, and row g (and g +
-// 8) of x, at the values of k that its codes stand for; the instruction's k
-// order is the codes' order, on both sides.
+// A step's codes come by one tensor copy (16 rows of 128 bytes, 16-byte units
+// swizzled by row), so that what is in flight costs neither registers nor the
+// warps' load path; its scales are 4 bytes a thread and row.
+//
+// One step: codes at `ws`, the block scales of k = 64 t .. 64 t + 63 of rows g
+// and g + 8 in s, x fragments at xs, 8 pieces of [rows][4] 16-byte units.  Thread
+// (g, t) multiplies weight rows g and g + 8, and row g (and g + 8) of x, at those
+// k; the instruction's k order is the codes' order, on both sides.
 template <int TOKS>
-__device__ __forceinline__ void multiply_step(float (&sum)[TOKS / 8][4], const Step& w,
-                                              uint32_t xs, int rows, int g, int t) {
-  float acc[2][TOKS / 8][4] = {};
+__device__ __forceinline__ void multiply_step(float (&sum)[Shape<TOKS>::TILES][4], uint32_t ws,
+                                              const uint32_t (&s)[2], uint32_t xs, int rows, int g,
+                                              int t) {
+  uint4 c[2][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      c[h][i] = lds128(ws + (g + 8 * h) * 128 + (((2 * t + i) ^ g) << 4));
+  float acc[2][Shape<TOKS>::TILES][4] = {};
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     uint32_t sc[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t pair = e4m3x2_to_f16(b < 2 ? w.s[h] & 0xFFFF : w.s[h] >> 16);
+      const uint32_t pair = e4m3x2_to_f16(b < 2 ? s[h] & 0xFFFF : s[h] >> 16);
       sc[h] = prmt(pair, pair, b % 2 ? 0x3232 : 0x1010);
     }
 #pragma unroll
     for (int p = 2 * b; p < 2 * b + 2; ++p) {
-      uint4 x[TOKS / 8];
+      uint4 x[Shape<TOKS>::TILES];
 #pragma unroll
-      for (int m = 0; m < TOKS / 8; ++m) {
+      for (int m = 0; m < Shape<TOKS>::TILES; ++m) {
         x[m] = make_uint4(0, 0, 0, 0);
         if (g + 8 * m < rows) x[m] = lds128(xs + ((p * rows + g + 8 * m) * 4 + t) * 16);
       }
       uint32_t v[2][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        e2m1x8_to_f16(word(w.c[h][p / 4], p % 4), v[h]);
+        e2m1x8_to_f16(word(c[h][p / 4], p % 4), v[h]);
 #pragma unroll
         for (int n = 0; n < 4; ++n) v[h][n] = mul_f16x2(v[h][n], sc[h]);
       }
 #pragma unroll
-      for (int m = 0; m < TOKS / 8; ++m) {
+      for (int m = 0; m < Shape<TOKS>::TILES; ++m) {
         mma_f16(acc[0][m], v[0][0], v[1][0], v[0][1], v[1][1], x[m].x, x[m].y);
         mma_f16(acc[1][m], v[0][2], v[1][2], v[0][3], v[1][3], x[m].z, x[m].w);
       }
@@ -154,7 +133,7 @@ __device__ __forceinline__ void multiply_step(float (&sum)[TOKS / 8][4], const S
   }
   // Sums of 128 terms at a time: the instruction cuts its sums off.
 #pragma unroll
-  for (int m = 0; m < TOKS / 8; ++m)
+  for (int m = 0; m < Shape<TOKS>::TILES; ++m)
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum[m][i] += acc[0][m][i] + acc[1][m][i];
 }
@@ -167,19 +146,24 @@ __device__ __forceinline__ void multiply_step(float (&sum)[TOKS / 8][4], const S
 // shared memory; when its places are full, or the rows of x change, they are
 // added in a fixed order, and those of a cluster's CTAs by its first one.
 template <int TOKS>
-__global__ void __launch_bounds__(32 * WARPS, 1)
-nvfp4_gemv_kernel(const GemvArgs a, const int tiles, const int cluster) {
+__global__ void __launch_bounds__(32 * WARPS, 2)
+nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, const int tiles,
+                  const int cluster, const int cap) {
+  using S = Shape<TOKS>;
+  constexpr int DEPTH = S::DEPTH, TILES = S::TILES;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align_up_shared<16>(smem_raw);
-  float* red = reinterpret_cast<float*>(smem);            // [item][warp][row][16]
-  const uint32_t xs = smem_addr(smem + SUM_BYTES);
+  uint8_t* smem = align_up_shared<1024>(smem_raw);
+  float* red = reinterpret_cast<float*>(smem + S::RING_BYTES);   // [item][warp][row][16]
+  const uint32_t xs = smem_addr(smem + S::RING_BYTES + SUM_BYTES);
   __shared__ uint32_t present[GEMV_EXPERTS_MAX / 32];
   __shared__ uint16_t active[GEMV_EXPERTS_MAX];           // the experts that have rows
   __shared__ int warp_sum[WARPS];
   __shared__ int list[TOKS + 2];                          // rows of the expert, their number, the next
-  __shared__ int best_of[TOKS / 8 * WARPS];
+  __shared__ int best_of[TILES * WARPS];
+  __shared__ uint64_t full[WARPS][DEPTH], empty[WARPS][DEPTH];   // of a part's places
   __shared__ int top[TOKS];                               // largest magnitude left of each row
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+  const int tid = threadIdx.x, lane = tid % 32, g = lane / 4, t = lane % 4;
+  const int warp = __shfl_sync(~0u, tid / 32, 0);          // the same for the warp, known to be
   const int rank = blockIdx.x % cluster;
   const int groups = (a.n + tiles * 16 - 1) / (tiles * 16);
 
@@ -240,38 +224,73 @@ nvfp4_gemv_kernel(const GemvArgs a, const int tiles, const int cluster) {
   };
   // K is staged in chunks of `room` at most (one, unless rows and K are both
   // large); a warp's steps in the chunk from k0 on start at start_of(k0).
-  constexpr int room = X_BYTES / (TOKS * 2) / STEP_K * STEP_K;
+  const int room = S::X_BYTES / (cap * 2) / STEP_K * STEP_K;
   const int turn = parts * STEP_K;
   auto start_of = [&](int k0) {
     const int behind = (k0 - k_first - part * STEP_K) % turn;
     return behind <= 0 ? k0 - behind : k0 + turn - behind;
   };
-  // This warp's loads: DEPTH steps (or places for them) at a time, in order over
-  // the chunks and the items.
-  const bool aligned = a.k % 64 == 0 && (reinterpret_cast<uintptr_t>(a.w_q) & 31) == 0;
-  const uint8_t *q[2] = {}, *s[2] = {};               // this thread's codes and scales at k = 0
-  int load_item = item_first, load_k0 = k_first, load_k = 0;
+  // A part's loads: DEPTH steps (or places for them) at a time, in order over the
+  // chunks and the items; its first warp asks for the codes of all its tiles in
+  // one copy (a copy takes 110 clocks to issue, 2 KB at a time 18 bytes a clock),
+  // each warp for its scales.
+  const uint32_t ring = smem_addr(smem) + part * (DEPTH * tiles * STEP_BYTES);
+  const uint32_t fulls = smem_addr(&full[part][0]), empties = smem_addr(&empty[part][0]);
+  if (tid < parts) {
+    for (int i = 0; i < DEPTH; ++i) {
+      mbar_init(smem_addr(&full[tid][i]), 1);
+      mbar_init(smem_addr(&empty[tid][i]), tiles);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const bool words = a.k % 64 == 0;                   // rows of scales start on 4 bytes
+  const uint8_t* s[2] = {};                           // this thread's scales at k = 0
+  int load_item = item_first, load_k0 = k_first, load_k = 0, load_row = 0;
+  uint32_t scale[DEPTH][2] = {};
+  uint32_t phase = 0, used = 0, pending = 0;          // a bit a place
+  bool ok = true;                                     // no wait ran out
   auto load_start = [&] {
     load_k = start_of(load_k0);
     if (load_item >= item_end) return;
     const Item item = item_at(load_item);
+    const int n = item.n0 + tile * 16;
+    load_row = item.e * a.n + item.n0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t n = static_cast<int64_t>(item.e) * a.n +
-                        min(item.n0 + tile * 16 + g + 8 * h, a.n - 1);
-      q[h] = a.w_q + n * (a.k / 2) + 32 * t;
-      s[h] = a.w_s + n * (a.k / 16) + 4 * t;
-    }
+    for (int h = 0; h < 2; ++h)
+      s[h] = a.w_s + (static_cast<int64_t>(item.e) * a.n + min(n + g + 8 * h, a.n - 1)) * (a.k / 16) +
+             4 * t;
   };
-  auto load_next = [&](Step& w, bool last) {          // last of DEPTH
+  auto load_next = [&](int i, uint32_t (&v)[2]) {
     const int k1 = min(load_k0 + room, k_end);
     if (load_item < item_end && load_k < k1) {
-      const uint8_t* const qk[2] = {q[0] + load_k / 2, q[1] + load_k / 2};
-      const uint8_t* const sk[2] = {s[0] + load_k / 16, s[1] + load_k / 16};
-      load_step(w, qk, sk, a.k - load_k - 64 * t, aligned);
+      if (tile == 0) {
+        // The place has been read by all the part's warps.
+        if (used >> i & 1) {
+          ok = ok && mbar_wait_bounded(empties + 8 * i, ~phase >> i & 1, a.timeout_ns);
+          __syncwarp();
+        }
+        if (elect_one()) {
+          mbar_arrive_expect_tx(fulls + 8 * i, tiles * STEP_BYTES);
+          tma_load_2d(ring + i * (tiles * STEP_BYTES), &codes, load_k / 2, load_row, fulls + 8 * i);
+        }
+      }
+      used |= 1u << i;
+      pending |= 1u << i;
+      const int left = a.k - load_k - 64 * t;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* p = s[h] + load_k / 16;
+        if (words && left >= 64) {
+          v[h] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        } else {
+          v[h] = left > 0 ? __ldg(reinterpret_cast<const uint16_t*>(p)) : 0;
+          if (left > 32) v[h] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + 1)) << 16;
+        }
+      }
     }
     load_k += turn;
-    if (last && load_k >= k1) {
+    if (i == DEPTH - 1 && load_k >= k1) {
       load_k0 += room;
       if (load_k0 >= k_end) {
         load_k0 = k_first;
@@ -280,16 +299,25 @@ nvfp4_gemv_kernel(const GemvArgs a, const int tiles, const int cluster) {
       load_start();
     }
   };
-  Step w[DEPTH] = {};
+  auto wait_for = [&](int i) {
+    ok = ok && mbar_wait_bounded(fulls + 8 * i, phase >> i & 1, a.timeout_ns);
+    phase ^= 1u << i;
+    pending &= ~(1u << i);
+    __syncwarp();
+  };
+  auto release = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empties + 8 * i);
+  };
   int held_item = -1, held_k0 = 0;                    // the chunk that they hold the start of
 
-  // Up to TOKS rows of expert e from row `from` on: `found` of them, row_at(i);
+  // Up to `cap` rows of expert e from row `from` on: `found` of them, row_at(i);
   // next_row is then the next one after them.
   int found = 0, next_row = 0, row0 = 0;
   auto list_rows = [&](int e, int from) {
     if (!a.experts) {
       row0 = from;
-      found = min(TOKS, a.rows - from);
+      found = min(cap, a.rows - from);
       next_row = from + found;
       return;
     }
@@ -300,11 +328,11 @@ nvfp4_gemv_kernel(const GemvArgs a, const int tiles, const int cluster) {
       while (at < a.rows && !past) {
         const int r = at + lane;
         const uint32_t hits = __ballot_sync(~0u, r < a.rows && a.experts[r] == e);
-        const int place = have + __popc(hits & ((1u << lane) - 1)), room = TOKS - have;
-        if ((hits >> lane & 1) && place < TOKS) list[place] = r;
-        past = __popc(hits) > room;
-        at += past ? static_cast<int>(__fns(hits, 0, room + 1)) : 32;
-        have = min(have + __popc(hits), TOKS);
+        const int place = have + __popc(hits & ((1u << lane) - 1)), free = cap - have;
+        if ((hits >> lane & 1) && place < cap) list[place] = r;
+        past = __popc(hits) > free;
+        at += past ? static_cast<int>(__fns(hits, 0, free + 1)) : 32;
+        have = min(have + __popc(hits), cap);
       }
       if (lane == 0) {
         list[TOKS] = have;
@@ -322,7 +350,7 @@ nvfp4_gemv_kernel(const GemvArgs a, const int tiles, const int cluster) {
   // where the multiplication reads it: first as they are, then, when the rows'
   // largest magnitudes below `below` are known, the window from there down as
   // f16.  True where smaller ones are left.
-  auto stage = [&](int rows, int k0, int k1, int (&below)[TOKS / 8]) {
+  auto stage = [&](int rows, int k0, int k1, int (&below)[TILES]) {
     const int all = (k1 - k0 + STEP_K - 1) / STEP_K * (STEP_K / 8);
     const int per = rows <= 1 ? 8 : rows <= 2 ? 4 : rows <= 4 ? 2 : 1;   // warps a row
     const int p0 = (warp % per) * 32 + lane;
@@ -333,7 +361,7 @@ nvfp4_gemv_kernel(const GemvArgs a, const int tiles, const int cluster) {
     if (again) __syncthreads();            // the last reads of what was staged before
     again = true;
 #pragma unroll
-    for (int i = 0; i < TOKS / 8; ++i) {
+    for (int i = 0; i < TILES; ++i) {
       const int m = warp / per + i * WARPS;
       if (m >= rows) break;
       const uint32_t lim = below[i] << 7;
@@ -358,7 +386,7 @@ nvfp4_gemv_kernel(const GemvArgs a, const int tiles, const int cluster) {
     __syncthreads();
     bool left = false;
 #pragma unroll
-    for (int i = 0; i < TOKS / 8; ++i) {
+    for (int i = 0; i < TILES; ++i) {
       const int m = warp / per + i * WARPS;
       if (m >= rows) break;
       const uint32_t lim = below[i] << 7;
@@ -442,23 +470,29 @@ nvfp4_gemv_kernel(const GemvArgs a, const int tiles, const int cluster) {
     const float global = a.w_global[here.e];
     while (true) {
       const int rows = found, after = next_row;
-      float out[TOKS / 8][4] = {};
+      float out[TILES][4] = {};
       for (int k0 = k_first; k0 < k_end; k0 += room) {
         const int k1 = min(k0 + room, k_end);
-        int below[TOKS / 8];                       // exponents still to take (this warp's rows)
+        int below[TILES];                          // exponents still to take (this warp's rows)
 #pragma unroll
-        for (int i = 0; i < TOKS / 8; ++i) below[i] = 256;
+        for (int i = 0; i < TILES; ++i) below[i] = 256;
         bool more = staged != k0;
         for (int window = 0; window == 0 || more; ++window) {
           if (more) {
             more = stage(rows, k0, k1, below);
             staged = window == 0 && !more ? k0 : -1;
           }
-          float sum[TOKS / 8][4] = {};
+          float sum[TILES][4] = {};
           // DEPTH steps at a time: each is multiplied and its place loaded again.
           // Where the places hold something else, the first round only loads.
           bool fill = item != held_item || k0 != held_k0;
           if (fill) {
+#pragma unroll 1
+            for (int i = 0; i < DEPTH; ++i)
+              if (pending >> i & 1) {
+                wait_for(i);
+                release(i);
+              }
             load_item = item;
             load_k0 = k0;
             load_start();
@@ -469,9 +503,13 @@ nvfp4_gemv_kernel(const GemvArgs a, const int tiles, const int cluster) {
             filled = fill;
 #pragma unroll
             for (int i = 0; i < DEPTH; ++i) {
-              if (!fill && k < k1)
-                multiply_step<TOKS>(sum, w[i], xs + (k - k0) * rows * 2, rows, g, t);
-              load_next(w[i], i == DEPTH - 1);
+              if (!fill && k < k1) {
+                wait_for(i);
+                multiply_step<TOKS>(sum, ring + (i * tiles + tile) * STEP_BYTES, scale[i],
+                                    xs + (k - k0) * rows * 2, rows, g, t);
+                release(i);
+              }
+              load_next(i, scale[i]);
               if (!fill) k += turn;
             }
             fill = false;
@@ -483,7 +521,7 @@ nvfp4_gemv_kernel(const GemvArgs a, const int tiles, const int cluster) {
           // To the output's units; both scales in one step, so that only a
           // result out of fp32's range leaves it.
 #pragma unroll
-          for (int m = 0; m < TOKS / 8; ++m)
+          for (int m = 0; m < TILES; ++m)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int r = 8 * m + 2 * t + i % 2;
@@ -493,15 +531,15 @@ nvfp4_gemv_kernel(const GemvArgs a, const int tiles, const int cluster) {
         }
       }
 #pragma unroll
-      for (int m = 0; m < TOKS / 8; ++m)
+      for (int m = 0; m < TILES; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 8 * m + 2 * t + i % 2;
           if (r < rows)
             red[(((item - first) * WARPS + warp) * rows + r) * 16 + g + 8 * (i / 2)] = out[m][i];
         }
-      const int room = SUM_BYTES / (WARPS * 16 * 4) / rows;      // items
-      if (after < a.rows || item + 1 - first == room || item + 1 == item_end) {
+      const int places = SUM_BYTES / (WARPS * 16 * 4) / rows;    // for items
+      if (after < a.rows || item + 1 - first == places || item + 1 == item_end) {
         flush(first, item + 1 - first, rows);
         first = item + 1;
       }
@@ -512,35 +550,42 @@ nvfp4_gemv_kernel(const GemvArgs a, const int tiles, const int cluster) {
       staged = -1;
     }
   }
+#pragma unroll 1
+  for (int i = 0; i < DEPTH; ++i)
+    if (pending >> i & 1) wait_for(i);
+  if (!ok && a.dev_err) atomicOr(a.dev_err, MXQ_DEVERR_TIMEOUT);
 }
 
-// How the work is cut: 16 * tiles output columns a CTA, K over clusters.
+// How the work is cut: 16 * tiles output columns a CTA, K over clusters, at most
+// `cap` rows of x at a time.
 struct Plan {
-  int tiles, cluster;
+  int tiles, cluster, cap;
 };
 
 // The plan with the least estimated time: a round of steps (256 x 16 weights
-// for each warp of the GPU) takes 0.45 us, a cluster's barriers 1 us for each
+// for each warp of the GPU) takes 0.8 us, a cluster's barriers 1 us for each
 // time that sums are added, and staging x 2 us and 0.02 us a thousand values.
-Plan choose(const GemvArgs& a, int rows, int64_t slots, int num_sms) {
+Plan choose(const GemvArgs& a, int rows, int toks, int x_bytes, int64_t slots, int num_sms) {
   const int64_t steps = (a.k + STEP_K - 1) / STEP_K;
-  Plan best{1, 1};
+  Plan best{1, 1, toks};
   double least = 1e30;
   for (int cluster = 1; cluster <= 8; cluster *= 2) {
     if (cluster > 1 && steps < cluster) break;
     const int64_t range = (steps + cluster - 1) / cluster;
     const double staging = 2 + 2e-5 * rows * range * STEP_K;
-    const bool fits = rows * range * STEP_K * 2 <= X_BYTES;
+    // Rows whose range of K is staged whole, if that takes all that are expected.
+    const int64_t fit = x_bytes / (2 * STEP_K) / (range > 0 ? range : 1);
+    const bool fits = fit >= rows;
     for (int tiles = 1; tiles <= WARPS; tiles *= 2) {
       const int parts = WARPS / tiles;
       const int64_t items = (a.n + tiles * 16 - 1) / (tiles * 16) * slots;
-      const int64_t at_once = num_sms / cluster;
+      const int64_t at_once = 2 * num_sms / cluster;
       const double turns = static_cast<double>((items + at_once - 1) / at_once);
-      const double item = 0.45 * ((range + parts - 1) / parts) + (cluster > 1 ? 1.0 : 0) + 0.1;
+      const double item = 0.8 * ((range + parts - 1) / parts) + (cluster > 1 ? 1.0 : 0) + 0.1;
       const double time = turns * (item + (fits ? 0 : staging)) + staging;
       if (time < least) {
         least = time;
-        best = {tiles, cluster};
+        best = {tiles, cluster, fits && fit < toks ? static_cast<int>(fit) : toks};
       }
     }
   }
@@ -548,15 +593,27 @@ Plan choose(const GemvArgs& a, int rows, int64_t slots, int num_sms) {
 }
 
 template <int TOKS>
-cudaError_t launch(const GemvArgs& a, Plan plan, int64_t slots, int num_sms,
+cudaError_t launch(const GemvArgs& a, int rows, int64_t slots, int num_sms,
                    cudaStream_t stream) {
-  constexpr int smem = X_BYTES + SUM_BYTES + 16;
+  constexpr int smem = Shape<TOKS>::SMEM;
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e =
       allow_shared(reinterpret_cast<const void*>(nvfp4_gemv_kernel<TOKS>), smem, &allowed);
   if (e != cudaSuccess) return e;
+  const Plan plan = choose(a, rows, TOKS, Shape<TOKS>::X_BYTES, slots, num_sms);
+  // w_q as rows of bytes, a copy of a line each of a CTA's rows.
+  CUtensorMap codes{};
+  if (a.k > 0) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.k / 2),
+                                static_cast<cuuint64_t>(a.num_experts) * a.n};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.k / 2)};
+    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(16 * plan.tiles)};
+    if (encode_map(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.w_q, dims, strides, box,
+                   CU_TENSOR_MAP_SWIZZLE_128B) != MXQ_OK)
+      return cudaErrorInvalidValue;
+  }
   const int64_t items = (a.n + plan.tiles * 16 - 1) / (plan.tiles * 16) * slots;
-  const int64_t most = num_sms / plan.cluster;
+  const int64_t most = 2 * num_sms / plan.cluster;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(items < most ? items : most) * plan.cluster);
   cfg.blockDim = dim3(32 * WARPS);
@@ -569,7 +626,8 @@ cudaError_t launch(const GemvArgs& a, Plan plan, int64_t slots, int num_sms,
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, nvfp4_gemv_kernel<TOKS>, a, plan.tiles, plan.cluster);
+  return cudaLaunchKernelEx(&cfg, nvfp4_gemv_kernel<TOKS>, codes, a, plan.tiles, plan.cluster,
+                            plan.cap);
 }
 
 }  // namespace
@@ -578,9 +636,8 @@ cudaError_t launch_nvfp4_gemv(const GemvArgs& a, int num_sms, cudaStream_t strea
   // At most this many experts have rows, and then this many rows each.
   const int64_t slots = !a.experts ? 1 : a.rows < a.num_experts ? a.rows : a.num_experts;
   const int rows = a.experts ? static_cast<int>((a.rows + slots - 1) / slots) : a.rows;
-  const Plan plan = choose(a, rows < 16 ? rows : 16, slots, num_sms);
-  return rows > 8 ? launch<16>(a, plan, slots, num_sms, stream)
-                  : launch<8>(a, plan, slots, num_sms, stream);
+  return rows > 8 ? launch<16>(a, rows < 16 ? rows : 16, slots, num_sms, stream)
+                  : launch<8>(a, rows, slots, num_sms, stream);
 }
 
 }  // namespace mxq
