@@ -106,24 +106,33 @@ struct Walk {
 };
 
 // 16 scale bytes from p on, of a row with `valid` bytes left, in a matrix that
-// ends at `end`.  Rows of scales start at any byte, so the bytes come from the
-// one or two 16-byte blocks around them; what follows the row's bytes is read
-// by no instruction.  Blocks that the matrix's end cuts are read by bytes.
-__device__ __forceinline__ uint4 load_scales(const uint8_t* p, int valid, const uint8_t* end) {
-  if (valid <= 0) return make_uint4(0, 0, 0, 0);
+// ends at `end`: as they lie, in the one or two 16-byte blocks around them (rows
+// of scales start at any byte).  What follows the row's bytes is read by no
+// instruction.  Blocks that the matrix's end cuts are read by bytes.
+__device__ __forceinline__ void load_scales(uint4& lo, uint4& hi, const uint8_t* p, int valid,
+                                            const uint8_t* end) {
   const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15;
-  const uint8_t* block = p - shift;
+  const uint4* block = reinterpret_cast<const uint4*>(p - shift);
   const bool two = shift + min(valid, 16) > 16;
-  if (block + (two ? 32 : 16) > end) {
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < valid) w[i / 4] |= static_cast<uint32_t>(__ldg(p + i)) << (8 * (i % 4));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+  const bool cut = reinterpret_cast<const uint8_t*>(block + (two ? 2 : 1)) > end;
+  lo = hi = make_uint4(0, 0, 0, 0);
+  if (valid > 0 && !cut) {
+    lo = __ldg(block);
+    if (two) hi = __ldg(block + 1);
   }
-  const uint4 lo = __ldg(reinterpret_cast<const uint4*>(block));
-  if (shift == 0) return lo;
-  const uint4 hi = two ? __ldg(reinterpret_cast<const uint4*>(block) + 1) : lo;
+  if (valid > 0 && cut) {
+    uint32_t w[8] = {};
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i >= shift && i < shift + min(valid, 16))
+        w[i / 4] |= static_cast<uint32_t>(__ldg(p - shift + i)) << (8 * (i % 4));
+    lo = make_uint4(w[0], w[1], w[2], w[3]);
+    hi = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// The 16 bytes from byte `shift` of two blocks on.
+__device__ __forceinline__ uint4 shift_scales(uint4 lo, uint4 hi, uint32_t shift) {
   uint32_t w[7] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z};
   if (shift & 8) {
 #pragma unroll
@@ -132,8 +141,7 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* p, int valid, const 
   }
   if (shift & 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = w[i + 1];
-    w[4] = w[5];
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
   }
   const uint32_t bits = 8 * (shift & 3);
   return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
@@ -179,24 +187,34 @@ __device__ __forceinline__ void store_patch(const GroupedArgs& a, uint32_t patch
     }
     return;
   }
-  for (int r = 0; r < rows; ++r) {
-    const uint32_t line = patch + r * 128;
-    if (a.out_f32) {
-      if (lane < cols) {
-        float v = __uint_as_float(lds32(line + (((lane / 4) ^ (r & 7)) << 4) + lane % 4 * 4));
-        float* p = static_cast<float*>(a.out) + (row + r) * a.ldo + col + lane;
-        *p = add ? v + *p : v;
-      }
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = lane + 32 * h;
-        const uint32_t v = lds32(line + (((c / 8) ^ (r & 7)) << 4) + c % 8 / 2 * 4);
-        if (c < cols)
-          static_cast<uint16_t*>(a.out)[(row + r) * a.ldo + col + c] =
-              static_cast<uint16_t>(v >> (16 * (c % 2)));
-      }
+  if (a.out_f32) {
+    const int unit = lane / 4, in = lane % 4 * 4;
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+      float v = __uint_as_float(lds32(patch + r * 128 + ((unit ^ (r & 7)) << 4) + in));
+      float* p = static_cast<float*>(a.out) + (row + r) * a.ldo + col + lane;
+      if (r < rows && lane < cols) *p = add ? v + *p : v;
     }
+    return;
+  }
+  // bf16: a lane a pair of columns that starts on 4 bytes, and in rows that start
+  // on an odd element the first and last column by themselves.
+#pragma unroll 4
+  for (int r = 0; r < 32; ++r) {
+    const int64_t first = (row + r) * a.ldo + col;
+    const int odd = static_cast<int>((reinterpret_cast<uintptr_t>(a.out) / 2 + first) & 1);
+    const uint32_t line = patch + r * 128;
+    uint32_t v = lds32(line + (((lane / 4) ^ (r & 7)) << 4) + lane % 4 * 4);
+    const uint32_t next = __shfl_down_sync(~0u, v, 1);
+    uint16_t* p = static_cast<uint16_t*>(a.out) + first;
+    if (r >= rows) continue;
+    if (odd && lane == 0 && cols > 0) p[0] = static_cast<uint16_t>(v);
+    if (odd) v = v >> 16 | next << 16;
+    const int c = 2 * lane + odd;
+    if (c + 1 < cols && c + 1 < 64)
+      stg32(p + c, v);
+    else if (c < cols && c < 64)
+      p[c] = static_cast<uint16_t>(v);
   }
 }
 
@@ -391,10 +409,14 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
     const int piece = tid % 4, r = (tid - 128) / 4;
     const uint8_t* a_end = a.a_s + static_cast<int64_t>(WGRAD ? a.a_rows : a.limit) * a.s_ld;
     const uint8_t* b_end = a.b_s + (WGRAD ? 1 : a.groups) * static_cast<int64_t>(a.b_rows) * a.s_ld;
-    uint4 v[1 + S::B_TILES][4];
+    uint4 v[1 + S::B_TILES][4], hi[1 + S::B_TILES][4];
+    const bool whole = a.s_ld % 16 == 0;     // every piece is a 16-byte block
     const uint8_t *ap = nullptr, *bp = nullptr;
     int at = 0, end = 0;             // scale bytes of the tile being loaded
     int a_left = 0, b_left = 0;      // rows from r on that exist
+    auto row_scales = [&](int b, int i) {
+      return b == 0 ? ap + i * 32 * a.s_ld : bp + ((b - 1) * 128 + i * 32) * a.s_ld;
+    };
     auto load = [&] {
       while (at >= end) {
         if (!walk.next(a, tile)) return false;
@@ -409,14 +431,18 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
       }
       // Pieces before the range are skipped like those after it.
       const int valid = at + 16 * piece + 16 > tile.first / 32 ? end - at - 16 * piece : 0;
+      // All loads are asked for before any is waited for.
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[0][i] = load_scales(ap + i * 32 * a.s_ld + at, 32 * i < a_left ? valid : 0, a_end);
+      for (int b = 0; b <= S::B_TILES; ++b)
 #pragma unroll
-        for (int b = 0; b < S::B_TILES; ++b)
-          v[1 + b][i] = load_scales(bp + (b * 128 + i * 32) * a.s_ld + at,
-                                    b * 128 + 32 * i < b_left ? valid : 0, b_end);
-      }
+        for (int i = 0; i < 4; ++i) {
+          const uint8_t* p = row_scales(b, i) + at;
+          const int has = (b == 0 ? 32 * i < a_left : (b - 1) * 128 + 32 * i < b_left) ? valid : 0;
+          if (whole)
+            v[b][i] = has > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+          else
+            load_scales(v[b][i], hi[b][i], p, has, b == 0 ? a_end : b_end);
+        }
       at += CHUNK * 4;
       return true;
     };
@@ -431,6 +457,13 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
       const uint32_t dst = scales + c * S::SCALE_BYTES + piece * 2048 + r * 16;
 #pragma unroll
       for (int b = 0; b <= S::B_TILES; ++b) {
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[b][i] = shift_scales(
+                v[b][i], hi[b][i],
+                static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row_scales(b, i))) & 15);
+        }
         const uint32_t to = dst + b * CHUNK * 512;
         sts128(to, v[b][0].x, v[b][1].x, v[b][2].x, v[b][3].x);
         sts128(to + 512, v[b][0].y, v[b][1].y, v[b][2].y, v[b][3].y);
