@@ -23,9 +23,9 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t SCALE_COL = 480;   // first tensor-memory column of the scales
 // Contraction values after which an fp32 output's sum is taken out of tensor
 // memory and added in fp32: the tensor cores cut their sums off instead of
-// rounding them, which is 1.3e-6 of the result after 14336 values and 2.7e-7
-// after this many.
-constexpr int SEGMENT = 4096;
+// rounding them, which is 6.4e-7 of the result after this many values, twice
+// that after twice as many.
+constexpr int SEGMENT = 8192;
 
 // A tile of ROWS * CTAS rows and BN columns, worked on by one CTA or a pair.
 template <int CTAS, int BN>
@@ -55,8 +55,7 @@ struct Tile {
   int g, m0, n0;
   int rows;         // rows of the group's output
   int first, end;   // contraction range
-  bool part;        // one of several ranges whose sums are added
-  bool add;         // to what an earlier range has written
+  bool add;         // to what an earlier range of the tile has written
 
   // Stages start on whole swizzle rows, so that their scales are whole words
   // and, where scale rows are multiples of 16 bytes, chunks whole 64-byte
@@ -87,7 +86,6 @@ struct Walk {
     tile.add = done > 0;
     tile.first = tile.add ? done : from;
     tile.end = a.out_f32 ? min(to, (tile.first / STEP_K + SEGMENT / STEP_K) * STEP_K) : to;
-    tile.part = tile.add || tile.end < to;
     constexpr int BAND = 2048 / (ROWS * CTAS);
     const int tiles_m = (tile.rows + ROWS * CTAS - 1) / (ROWS * CTAS);
     int i = t - start[g];
@@ -488,9 +486,11 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
                                              : static_cast<int64_t>(off[tile.g]));
       const uint32_t s = acc % 2;
       const bool empty_tile = tile.first == tile.end;
-      // Whole patches leave by bulk copies, clipped at the output's last column;
-      // those with rows of the next group, and sums to be added, by threads.
-      const bool bulk = a.out_vec && !tile.part && (WGRAD ? rows > 0 : rows == 32);
+      // Whole patches leave by bulk copies, clipped at the output's last column
+      // (later ranges are added there: what a warp has written before is
+      // complete); those with rows of the next group, by threads.
+      const bool bulk = a.out_vec && (WGRAD ? rows > 0 : rows == 32);
+      if (tile.add && lane == 0) bulk_wait_all();
       if (!empty_tile) {
         if (!mbar_wait_bounded(acc_full + 8 * s, (acc / 2) & 1, a.timeout_ns)) {
           ok = false;
@@ -499,8 +499,25 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
         tc_fence_after_sync();
         ++acc;
       }
-      const uint32_t base = tmem + S::acc_col(s) + (static_cast<uint32_t>(warp) << 21);
       const int width = a.out_f32 ? 32 : 64;             // columns of a patch
+      if (empty_tile && bulk) {
+        // One patch of zeros for all the columns.
+        const uint32_t patch = patches + (warp * S::PATCHES + turn++ % S::PATCHES) * 4096;
+        if (lane == 0) bulk_wait_read<S::PATCHES - 1>();
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 8; ++u) sts128(patch + u * 512 + lane * 16, 0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          for (int j = 0; j < BN && tile.n0 + j < a.b_rows; j += width)
+            tma_store_3d(&maps.out, patch, tile.n0 + j, WGRAD ? first : static_cast<int>(out_row),
+                         WGRAD ? tile.g : 0);
+          bulk_commit();
+        }
+        continue;
+      }
+      const uint32_t base = tmem + S::acc_col(s) + (static_cast<uint32_t>(warp) << 21);
       for (int i = 0; i < BN; i += width) {
         // Accumulator 0 shares its last 32 columns with the next tile's
         // first 32: they are read first.
@@ -546,8 +563,9 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
           store_patch(a, patch, lane, out_row, rows, tile.n0 + j, a.b_rows - tile.n0 - j,
                       tile.add);
         } else if (lane == 0 && tile.n0 + j < a.b_rows) {
-          tma_store_3d(&maps.out, patch, tile.n0 + j, WGRAD ? first : static_cast<int>(out_row),
-                       WGRAD ? tile.g : 0);
+          const int y = WGRAD ? first : static_cast<int>(out_row), z = WGRAD ? tile.g : 0;
+          if (tile.add) tma_add_3d(&maps.out, patch, tile.n0 + j, y, z);
+          else tma_store_3d(&maps.out, patch, tile.n0 + j, y, z);
         }
         if (lane == 0) bulk_commit();       // one group a patch, empty ones too
       }

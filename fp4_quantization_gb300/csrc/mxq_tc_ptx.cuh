@@ -219,6 +219,14 @@ __device__ __forceinline__ bool mbar_wait_bounded_cluster(uint32_t bar, uint32_t
   }
 }
 
+// 3-D TMA tile store that adds fp32 values to what is there.
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src, int x, int y,
+                                           int z) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];"
+      :: "l"(map), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
+}
+
 // 2-D TMA tile load into this CTA's shared memory, completing on a barrier of
 // the pair's first CTA (an address of cluster_addr).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x,

@@ -247,7 +247,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
   const bool words = a.k % 64 == 0;                   // rows of scales start on 4 bytes
   const uint8_t* s[2] = {};                           // this thread's scales at k = 0
   int load_item = item_first, load_k0 = k_first, load_k = 0, load_row = 0;
-  uint32_t scale[DEPTH][2] = {};
+  uint32_t scale[DEPTH][2][2] = {};                   // four scales a row, or two and two
   uint32_t phase = 0, used = 0, pending = 0;          // a bit a place
   bool ok = true;                                     // no wait ran out
   auto load_start = [&] {
@@ -261,7 +261,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
       s[h] = a.w_s + (static_cast<int64_t>(item.e) * a.n + min(n + g + 8 * h, a.n - 1)) * (a.k / 16) +
              4 * t;
   };
-  auto load_next = [&](int i, uint32_t (&v)[2]) {
+  auto load_next = [&](int i, uint32_t (&v)[2][2]) {
     const int k1 = min(load_k0 + room, k_end);
     if (load_item < item_end && load_k < k1) {
       if (tile == 0) {
@@ -282,10 +282,11 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
       for (int h = 0; h < 2; ++h) {
         const uint8_t* p = s[h] + load_k / 16;
         if (words && left >= 64) {
-          v[h] = __ldg(reinterpret_cast<const uint32_t*>(p));
+          v[h][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
         } else {
-          v[h] = left > 0 ? __ldg(reinterpret_cast<const uint16_t*>(p)) : 0;
-          if (left > 32) v[h] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + 1)) << 16;
+          const uint16_t* two = reinterpret_cast<const uint16_t*>(p);
+          v[h][0] = left > 0 ? __ldg(two) : 0;
+          v[h][1] = left > 32 ? __ldg(two + 1) : 0;
         }
       }
     }
@@ -505,7 +506,9 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
             for (int i = 0; i < DEPTH; ++i) {
               if (!fill && k < k1) {
                 wait_for(i);
-                multiply_step<TOKS>(sum, ring + (i * tiles + tile) * STEP_BYTES, scale[i],
+                const uint32_t four[2] = {words ? scale[i][0][0] : scale[i][0][0] | scale[i][0][1] << 16,
+                                          words ? scale[i][1][0] : scale[i][1][0] | scale[i][1][1] << 16};
+                multiply_step<TOKS>(sum, ring + (i * tiles + tile) * STEP_BYTES, four,
                                     xs + (k - k0) * rows * 2, rows, g, t);
                 release(i);
               }

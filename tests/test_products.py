@@ -99,6 +99,7 @@ GEMM = [
     ("odd", [127, 129, 1, 255, 64], 1001, 1056, 0, 0),
     ("outside_rows", [5, 300], 130, 544, 7, 200),
     ("long_k", [40, 200], 72, 8192 + 32, 0, 0),
+    ("ranges", [33, 130], 160, 3 * 8192 - 64, 0, 0),
     ("chunk_edges", [128, 256, 384], 384, 512, 0, 0),
     ("many_tiles", [700, 90, 2000, 1310], 1400, 736, 0, 0),
     ("many_groups", [(i * 37) % 23 for i in range(300)], 48, 224, 0, 0),
@@ -203,6 +204,7 @@ WGRAD = [
     ("odd_widths", [96, 160, 32, 512], 257, 301, 0, 0),
     ("outside_rows", [64, 96], 64, 96, 32, 160),
     ("long", [4096, 32, 2080], 136, 264, 0, 0),
+    ("ranges", [96, 20000, 8192, 32], 264, 136, 0, 0),
     ("scale_alignment", [32 * i for i in (1, 2, 3, 5, 7, 11, 13, 4)], 96, 160, 0, 32),
     ("many_tiles", [256, 320], 1500, 1100, 0, 0),
     ("wide_pairs", [224, 0, 800], 2048, 2304, 0, 0),
