@@ -161,7 +161,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
   __shared__ int list[TOKS + 2];                          // rows of the expert, their number, the next
   __shared__ int best_of[TILES * WARPS];
   __shared__ uint64_t full[WARPS][DEPTH], empty[WARPS][DEPTH];   // of a part's places
-  __shared__ int top[TOKS];                               // largest magnitude left of each row
+  __shared__ float2 unit[TOKS];                           // what a sum of staged row i is multiplied by
   const int tid = threadIdx.x, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int warp = __shfl_sync(~0u, tid / 32, 0);          // the same for the warp, known to be
   const int rank = blockIdx.x % cluster;
@@ -351,7 +351,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
   // where the multiplication reads it: first as they are, then, when the rows'
   // largest magnitudes below `below` are known, the window from there down as
   // f16.  True where smaller ones are left.
-  auto stage = [&](int rows, int k0, int k1, int (&below)[TILES]) {
+  auto stage = [&](int rows, int k0, int k1, float global, int (&below)[TILES]) {
     const int all = (k1 - k0 + STEP_K - 1) / STEP_K * (STEP_K / 8);
     const int per = rows <= 1 ? 8 : rows <= 2 ? 4 : rows <= 4 ? 2 : 1;   // warps a row
     const int p0 = (warp % per) * 32 + lane;
@@ -393,8 +393,17 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
       const uint32_t lim = below[i] << 7;
       int most = lane < per ? best_of[i * WARPS + warp / per * per + lane] : 0;
       most = __reduce_max_sync(~0u, most);
-      if (lane == 0) top[m] = most;        // the same from each of the row's warps
       const int high = most >> 7;
+      if (lane == 0) {                     // the same from each of the row's warps
+        // G_e over the rows' factor; both in one step and the powers of two apart,
+        // so that only a result out of fp32's range leaves it.
+        int n;
+        const float frac = frexpf(global, &n);
+        n -= min(141 - high, 127);
+        const int n1 = max(-125, min(n, 127)), n2 = max(-126, min(n - n1, 127));
+        unit[m] = make_float2(frac * __int_as_float((n1 + 127) << 23),
+                              __int_as_float((n2 + 127) << 23));
+      }
       const uint32_t low = max(high - 28, 0) << 7;
       const float up = __uint_as_float(static_cast<uint32_t>(min(141 - high, 127) + 127) << 23);
 #pragma unroll 1
@@ -480,7 +489,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
         bool more = staged != k0;
         for (int window = 0; window == 0 || more; ++window) {
           if (more) {
-            more = stage(rows, k0, k1, below);
+            more = stage(rows, k0, k1, global, below);
             staged = window == 0 && !more ? k0 : -1;
           }
           float sum[TILES][4] = {};
@@ -519,17 +528,13 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
           } while (filled || k < k1);
           held_item = k0 + room < k_end ? item : item + 1;     // what the loads have begun
           held_k0 = k0 + room < k_end ? k0 + room : k_first;
-          int exp_g;
-          const float frac_g = frexpf(global, &exp_g);
-          // To the output's units; both scales in one step, so that only a
-          // result out of fp32's range leaves it.
+          // To the output's units.
 #pragma unroll
           for (int m = 0; m < TILES; ++m)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int r = 8 * m + 2 * t + i % 2;
-              const int high = r < rows ? top[r] >> 7 : 0;
-              out[m][i] += ldexpf(sum[m][i] * frac_g, exp_g - min(141 - high, 127));
+              if (r < rows) out[m][i] += sum[m][i] * unit[r].x * unit[r].y;
             }
         }
       }
@@ -565,34 +570,27 @@ struct Plan {
   int tiles, cluster, cap;
 };
 
-// The plan with the least estimated time: a round of steps (256 x 16 weights
-// for each warp of the GPU) takes 0.8 us, a cluster's barriers 1 us for each
-// time that sums are added, and staging x 2 us and 0.02 us a thousand values.
+// Tiles of 8 * 16 columns wherever they make items enough for three CTAs on two
+// SMs: a part of K less is a copy less, and sums less to add.  Where they do
+// not, K is split: inside the CTA for one or two rows (28672 x 8192 weights, one
+// row: 34 us in halves, 38 whole, 36 over clusters of two), over clusters for
+// more, whose staged rows the CTAs of a cluster then share out (4099 x 11008,
+// thirteen rows: 22 us over clusters of 8, 84 in one CTA, 34 in halves).
 Plan choose(const GemvArgs& a, int rows, int toks, int x_bytes, int64_t slots, int num_sms) {
   const int64_t steps = (a.k + STEP_K - 1) / STEP_K;
-  Plan best{1, 1, toks};
-  double least = 1e30;
-  for (int cluster = 1; cluster <= 8; cluster *= 2) {
-    if (cluster > 1 && steps < cluster) break;
-    const int64_t range = (steps + cluster - 1) / cluster;
-    const double staging = 2 + 2e-5 * rows * range * STEP_K;
-    // Rows whose range of K is staged whole, if that takes all that are expected.
-    const int64_t fit = x_bytes / (2 * STEP_K) / (range > 0 ? range : 1);
-    const bool fits = fit >= rows;
-    for (int tiles = 1; tiles <= WARPS; tiles *= 2) {
-      const int parts = WARPS / tiles;
-      const int64_t items = (a.n + tiles * 16 - 1) / (tiles * 16) * slots;
-      const int64_t at_once = 2 * num_sms / cluster;
-      const double turns = static_cast<double>((items + at_once - 1) / at_once);
-      const double item = 0.8 * ((range + parts - 1) / parts) + (cluster > 1 ? 1.0 : 0) + 0.1;
-      const double time = turns * (item + (fits ? 0 : staging)) + staging;
-      if (time < least) {
-        least = time;
-        best = {tiles, cluster, fits && fit < toks ? static_cast<int>(fit) : toks};
-      }
-    }
-  }
-  return best;
+  auto items = [&](int tiles) { return (a.n + tiles * 16 - 1) / (tiles * 16) * slots; };
+  Plan plan{WARPS, 1, toks};
+  const int64_t want = num_sms * 3 / 2;
+  while (rows <= 2 && plan.tiles > 1 && items(plan.tiles) < want) plan.tiles /= 2;
+  while (plan.cluster < 8 && items(plan.tiles) * plan.cluster < want &&
+         steps >= 2 * plan.cluster * (WARPS / plan.tiles))
+    plan.cluster *= 2;
+  while (plan.tiles > 1 && items(plan.tiles) * plan.cluster < num_sms / 2) plan.tiles /= 2;
+  // Rows whose range of K is staged whole, if that takes all that are expected.
+  const int64_t range = (steps + plan.cluster - 1) / plan.cluster;
+  const int64_t fit = x_bytes / (2 * STEP_K) / (range > 0 ? range : 1);
+  if (fit >= rows && fit < toks) plan.cap = static_cast<int>(fit);
+  return plan;
 }
 
 template <int TOKS>
