@@ -20,6 +20,7 @@ constexpr int STEP_K = 128;           // contraction bytes of one pipeline stage
 constexpr int CHUNK = 16;
 constexpr int THREADS = 320;          // 4 epilogue, 4 scale, 1 copy, 1 issuing warp
 constexpr uint32_t TMEM_COLS = 512;
+constexpr int FEW_ROWS = 32;          // rows of a group on average up to which they are B
 constexpr uint32_t SCALE_COL = 480;   // first tensor-memory column of the scales
 // Contraction values after which an fp32 output's sum is taken out of tensor
 // memory and added in fp32: the tensor cores cut their sums off instead of
@@ -27,19 +28,27 @@ constexpr uint32_t SCALE_COL = 480;   // first tensor-memory column of the scale
 // that after twice as many.
 constexpr int SEGMENT = 8192;
 
+// What the two operands and the output tile are.
+//  FORWARD: A the rows of x of a group, B its expert's weight.
+//  FEW:     A the weight, B the rows of x: the tile is the output's transpose.
+//           Few rows fill a fraction of a 128-row operand, and its other rows
+//           would be half of all that is copied; here they are the narrow one.
+//  WGRAD:   A the gradient, B x, both along the group's rows.
+enum Kind { FORWARD, FEW, WGRAD };
+
 // A tile of ROWS * CTAS rows and BN columns, worked on by one CTA or a pair.
 template <int CTAS, int BN>
 struct Shape {
   static constexpr int A_BYTES = ROWS * STEP_K;
   static constexpr int B_ROWS = BN / CTAS;                          // of each CTA
   static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * STEP_K;
-  static constexpr int STAGES = STAGE_BYTES > 40 * 1024 ? 3 : 4;
+  static constexpr int STAGES = STAGE_BYTES > 40 * 1024 ? 3 : BN >= 128 ? 4 : 8;
   static constexpr int B_TILES = (BN + 127) / 128;                  // scale tiles of B a stage
   static constexpr int SCALE_BYTES = CHUNK * 512 * (1 + B_TILES);   // one scale chunk
   static constexpr int SCALE_CHUNKS = 2;
   // Patches of 32 rows x 128 bytes that the epilogue's four warps stage: two
   // each, one filled while the other leaves (one where shared memory is short).
-  static constexpr int PATCHES = STAGE_BYTES > 40 * 1024 ? 1 : 2;
+  static constexpr int PATCHES = BN < 128 ? 0 : STAGE_BYTES > 40 * 1024 ? 1 : 2;
   static constexpr int OUT_BYTES = 4 * PATCHES * 4096;
   // Column of accumulator s.  Two 256-column accumulators share 32 columns.
   static constexpr uint32_t acc_col(uint32_t s) { return s * (BN == 256 ? 224 : BN); }
@@ -50,12 +59,14 @@ struct Shape {
 };
 
 // Where a tile lies: its group, its first row and column in the group's
-// output, the group's rows, and the tile's contraction range.
+// product, that product's rows and columns, and the tile's contraction range.
 struct Tile {
   int g, m0, n0;
-  int rows;         // rows of the group's output
+  int rows, cols;
   int first, end;   // contraction range
   bool add;         // to what an earlier range of the tile has written
+  int ay, az;       // the product's first row in A: row ay of matrix az,
+  int by, bz;       // and its first column in B
 
   // Stages start on whole swizzle rows, so that their scales are whole words
   // and, where scale rows are multiples of 16 bytes, chunks whole 64-byte
@@ -68,12 +79,13 @@ struct Tile {
 
 // Walks the tiles of this CTA (or pair) in order.  Inside a group the row
 // tiles of a band of 2048 rows run fastest, so a wave's tiles share their rows
-// and each column tile's codes come from memory once a band.
-template <int CTAS, int BN, bool WGRAD>
+// and each column tile's codes come from memory once a band; with few rows of
+// x, all of them beside each weight tile.
+template <int CTAS, int BN, int KIND>
 struct Walk {
   const int* off;
   const int* start;     // first tile of each group, and the total
-  int groups, tiles_n;
+  int groups;
   int t, g, done;       // done: where tile t's next contraction range starts, or 0
 
   __device__ __forceinline__ bool next(const GroupedArgs& a, Tile& tile) {
@@ -81,19 +93,30 @@ struct Walk {
     while (t >= start[g + 1]) ++g;
     const int lo = off[g], rows_g = off[g + 1] - lo;
     tile.g = g;
-    tile.rows = WGRAD ? a.a_rows : rows_g;
-    const int from = WGRAD ? lo : 0, to = WGRAD ? lo + rows_g : a.depth;
+    tile.rows = KIND == FORWARD ? rows_g : a.a_rows;
+    tile.cols = KIND == FEW ? rows_g : a.b_rows;
+    tile.ay = KIND == FORWARD ? lo : 0;
+    tile.az = KIND == FEW ? g : 0;
+    tile.by = KIND == FEW ? lo : 0;
+    tile.bz = KIND == FORWARD ? g : 0;
+    const int from = KIND == WGRAD ? lo : 0, to = KIND == WGRAD ? lo + rows_g : a.depth;
     tile.add = done > 0;
     tile.first = tile.add ? done : from;
     tile.end = a.out_f32 ? min(to, (tile.first / STEP_K + SEGMENT / STEP_K) * STEP_K) : to;
-    constexpr int BAND = 2048 / (ROWS * CTAS);
-    const int tiles_m = (tile.rows + ROWS * CTAS - 1) / (ROWS * CTAS);
+    const int tiles_n = (tile.cols + BN - 1) / BN;
     int i = t - start[g];
-    const int band = i / (BAND * tiles_n);
-    i -= band * BAND * tiles_n;
-    const int height = min(BAND, tiles_m - band * BAND);
-    tile.m0 = (band * BAND + i % height) * (ROWS * CTAS);
-    tile.n0 = i / height * BN;
+    if constexpr (KIND == FEW) {
+      tile.m0 = i / tiles_n * (ROWS * CTAS);
+      tile.n0 = i % tiles_n * BN;
+    } else {
+      constexpr int BAND = 2048 / (ROWS * CTAS);
+      const int tiles_m = (tile.rows + ROWS * CTAS - 1) / (ROWS * CTAS);
+      const int band = i / (BAND * tiles_n);
+      i -= band * BAND * tiles_n;
+      const int height = min(BAND, tiles_m - band * BAND);
+      tile.m0 = (band * BAND + i % height) * (ROWS * CTAS);
+      tile.n0 = i / height * BN;
+    }
     done = tile.end;
     if (done == to) {
       done = 0;
@@ -216,7 +239,7 @@ __device__ __forceinline__ void store_patch(const GroupedArgs& a, uint32_t patch
   }
 }
 
-template <int CTAS, int BN, bool WGRAD>
+template <int CTAS, int BN, int KIND>
 __global__ void __launch_bounds__(THREADS, 1)
 mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a) {
   using S = Shape<CTAS, BN>;
@@ -237,7 +260,6 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
 
   const int tid = threadIdx.x, lane = tid % 32;
   const int warp = __shfl_sync(~0u, tid / 32, 0);          // the same for the warp, known to be
-  const int tiles_n = (a.b_rows + BN - 1) / BN;
   const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;   // 0: the CTA that issues
 
   // full, sc_full and acc_empty are waited on by the issuing CTA alone, and
@@ -267,7 +289,7 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
   for (int i = tid; i <= a.groups; i += THREADS) {
     const int v = a.offsets[i];
     const int before = i > 0 ? a.offsets[i - 1] : 0;
-    bad |= v < before || v > a.limit || (WGRAD && v % 32 != 0);
+    bad |= v < before || v > a.limit || (KIND == WGRAD && v % 32 != 0);
     off[i] = v;
   }
   bad = __syncthreads_or(bad);
@@ -276,8 +298,9 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
     for (int i = 0; i < a.groups; i += 32) {
       int n = 0;
       if (!bad && i + lane < a.groups) {
-        const int rows = WGRAD ? a.a_rows : off[i + lane + 1] - off[i + lane];
-        n = (rows + ROWS * CTAS - 1) / (ROWS * CTAS) * tiles_n;
+        const int rows_g = off[i + lane + 1] - off[i + lane];
+        const int rows = KIND == FORWARD ? rows_g : a.a_rows, cols = KIND == FEW ? rows_g : a.b_rows;
+        n = (rows + ROWS * CTAS - 1) / (ROWS * CTAS) * ((cols + BN - 1) / BN);
       }
       int sum = n;
 #pragma unroll
@@ -297,7 +320,7 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
-  Walk<CTAS, BN, WGRAD> walk{off, start, a.groups, tiles_n, static_cast<int>(blockIdx.x) / CTAS, 0, 0};
+  Walk<CTAS, BN, KIND> walk{off, start, a.groups, static_cast<int>(blockIdx.x) / CTAS, 0, 0};
   Tile tile;
   bool ok = true;
 
@@ -306,9 +329,8 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
     if (elect_one()) {
       uint32_t it = 0;
       while (ok && walk.next(a, tile)) {
-        const int ay = (WGRAD ? 0 : off[tile.g]) + tile.m0 + static_cast<int>(rank) * ROWS;
-        const int by = tile.n0 + static_cast<int>(rank) * S::B_ROWS;
-        const int bz = WGRAD ? 0 : tile.g;
+        const int ay = tile.ay + tile.m0 + static_cast<int>(rank) * ROWS;
+        const int by = tile.by + tile.n0 + static_cast<int>(rank) * S::B_ROWS;
         for (int k = tile.step0(); k < tile.step1(); ++k, ++it) {
           const uint32_t s = it % S::STAGES;
           if (it >= S::STAGES &&
@@ -321,11 +343,11 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
           const int x = k * STEP_K;
           if constexpr (CTAS == 2) {
             const uint32_t there = cluster_addr(bar, 0);
-            tma_load_2d_pair(dst, &maps.a, x, ay, there);
-            tma_load_3d_pair(dst + S::A_BYTES, &maps.b, x, by, bz, there);
+            tma_load_3d_pair(dst, &maps.a, x, ay, tile.az, there);
+            tma_load_3d_pair(dst + S::A_BYTES, &maps.b, x, by, tile.bz, there);
           } else {
-            tma_load_2d(dst, &maps.a, x, ay, bar);
-            tma_load_3d(dst + S::A_BYTES, &maps.b, x, by, bz, bar);
+            tma_load_3d(dst, &maps.a, x, ay, tile.az, bar);
+            tma_load_3d(dst + S::A_BYTES, &maps.b, x, by, tile.bz, bar);
           }
         }
       }
@@ -405,8 +427,12 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
     // and a thread's rows one 16-byte unit of each stage's tile.  The loads run
     // a chunk before the stores, over the ends of tiles too. ----
     const int piece = tid % 4, r = (tid - 128) / 4;
-    const uint8_t* a_end = a.a_s + static_cast<int64_t>(WGRAD ? a.a_rows : a.limit) * a.s_ld;
-    const uint8_t* b_end = a.b_s + (WGRAD ? 1 : a.groups) * static_cast<int64_t>(a.b_rows) * a.s_ld;
+    const int64_t a_total = KIND == FORWARD ? a.limit
+                            : KIND == FEW   ? static_cast<int64_t>(a.groups) * a.a_rows : a.a_rows;
+    const int64_t b_total = KIND == FORWARD ? static_cast<int64_t>(a.groups) * a.b_rows
+                            : KIND == FEW   ? a.limit : a.b_rows;
+    const uint8_t* a_end = a.a_s + a_total * a.s_ld;
+    const uint8_t* b_end = a.b_s + b_total * a.s_ld;
     uint4 v[1 + S::B_TILES][4], hi[1 + S::B_TILES][4];
     const bool whole = a.s_ld % 16 == 0;     // every piece is a 16-byte block
     const uint8_t *ap = nullptr, *bp = nullptr;
@@ -422,9 +448,9 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
         at = tile.step0() / CHUNK * (CHUNK * 4);
         end = tile.first < tile.end ? tile.end / 32 : at;
         a_left = tile.rows - row;
-        b_left = a.b_rows - tile.n0 - r;
-        ap = a.a_s + ((WGRAD ? 0 : static_cast<int64_t>(off[tile.g])) + row) * a.s_ld + 16 * piece;
-        bp = a.b_s + ((WGRAD ? 0 : static_cast<int64_t>(tile.g) * a.b_rows) + tile.n0 + r) * a.s_ld +
+        b_left = min(tile.cols - tile.n0, BN) - r;
+        ap = a.a_s + (static_cast<int64_t>(tile.az) * a.a_rows + tile.ay + row) * a.s_ld + 16 * piece;
+        bp = a.b_s + (static_cast<int64_t>(tile.bz) * a.b_rows + tile.by + tile.n0 + r) * a.s_ld +
              16 * piece;
       }
       // Pieces before the range are skipped like those after it.
@@ -482,14 +508,14 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
     while (ok && walk.next(a, tile)) {
       const int first = tile.m0 + static_cast<int>(rank) * ROWS + warp * 32;
       const int rows = min(32, tile.rows - first);       // may be negative
-      const int64_t out_row = first + (WGRAD ? static_cast<int64_t>(tile.g) * a.a_rows
-                                             : static_cast<int64_t>(off[tile.g]));
+      const int64_t out_row = first + (KIND == WGRAD ? static_cast<int64_t>(tile.g) * a.a_rows
+                                                     : static_cast<int64_t>(tile.ay));
       const uint32_t s = acc % 2;
       const bool empty_tile = tile.first == tile.end;
       // Whole patches leave by bulk copies, clipped at the output's last column
       // (later ranges are added there: what a warp has written before is
       // complete); those with rows of the next group, by threads.
-      const bool bulk = a.out_vec && (WGRAD ? rows > 0 : rows == 32);
+      const bool bulk = KIND != FEW && a.out_vec && (KIND == WGRAD ? rows > 0 : rows == 32);
       if (tile.add && lane == 0) bulk_wait_all();
       if (!empty_tile) {
         if (!mbar_wait_bounded(acc_full + 8 * s, (acc / 2) & 1, a.timeout_ns)) {
@@ -499,20 +525,51 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
         tc_fence_after_sync();
         ++acc;
       }
+      if constexpr (KIND == FEW) {
+        // The lanes hold 32 neighbouring columns of a row of the output, row by row.
+        const uint32_t from = tmem + S::acc_col(s) + (static_cast<uint32_t>(warp) << 21);
+#pragma unroll 1
+        for (int j = 0; j < BN; j += 32) {
+          uint32_t v[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = 0;
+          if (!empty_tile) {
+            tmem_load_x32(from + j, v);
+            tmem_wait_load();
+          }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (!empty_tile && lane == 0 && j == BN - 32) mbar_arrive(acc_empty + 8 * s);
+          const int count = lane < rows ? tile.cols - tile.n0 - j : 0;
+          const int64_t at = (static_cast<int64_t>(tile.by) + tile.n0 + j) * a.ldo + first + lane;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (c >= count) continue;
+            if (a.out_f32) {
+              float* p = static_cast<float*>(a.out) + at + c * a.ldo;
+              *p = tile.add ? __uint_as_float(v[c]) + *p : __uint_as_float(v[c]);
+            } else {
+              static_cast<uint16_t*>(a.out)[at + c * a.ldo] =
+                  static_cast<uint16_t>(pack_bf16(__uint_as_float(v[c]), 0.f));
+            }
+          }
+        }
+        continue;
+      }
       const int width = a.out_f32 ? 32 : 64;             // columns of a patch
       if (empty_tile && bulk) {
         // One patch of zeros for all the columns.
-        const uint32_t patch = patches + (warp * S::PATCHES + turn++ % S::PATCHES) * 4096;
-        if (lane == 0) bulk_wait_read<S::PATCHES - 1>();
+        const uint32_t patch = patches + (warp * S::PATCHES + turn++ % (S::PATCHES ? S::PATCHES : 1)) * 4096;
+        if (lane == 0) bulk_wait_read<S::PATCHES ? S::PATCHES - 1 : 0>();
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < 8; ++u) sts128(patch + u * 512 + lane * 16, 0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          for (int j = 0; j < BN && tile.n0 + j < a.b_rows; j += width)
-            tma_store_3d(&maps.out, patch, tile.n0 + j, WGRAD ? first : static_cast<int>(out_row),
-                         WGRAD ? tile.g : 0);
+          for (int j = 0; j < BN && tile.n0 + j < tile.cols; j += width)
+            tma_store_3d(&maps.out, patch, tile.n0 + j, KIND == WGRAD ? first : static_cast<int>(out_row),
+                         KIND == WGRAD ? tile.g : 0);
           bulk_commit();
         }
         continue;
@@ -522,8 +579,8 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
         // Accumulator 0 shares its last 32 columns with the next tile's
         // first 32: they are read first.
         const int j = BN == 256 && s == 0 ? BN - width - i : i;
-        const uint32_t patch = patches + (warp * S::PATCHES + turn++ % S::PATCHES) * 4096;
-        if (lane == 0) bulk_wait_read<S::PATCHES - 1>();
+        const uint32_t patch = patches + (warp * S::PATCHES + turn++ % (S::PATCHES ? S::PATCHES : 1)) * 4096;
+        if (lane == 0) bulk_wait_read<S::PATCHES ? S::PATCHES - 1 : 0>();
         __syncwarp();
         for (int h = 0; h < width / 32; ++h) {
           uint32_t v[32];
@@ -560,10 +617,10 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
           else mbar_arrive(acc_empty + 8 * s);
         }
         if (!bulk) {
-          store_patch(a, patch, lane, out_row, rows, tile.n0 + j, a.b_rows - tile.n0 - j,
+          store_patch(a, patch, lane, out_row, rows, tile.n0 + j, tile.cols - tile.n0 - j,
                       tile.add);
-        } else if (lane == 0 && tile.n0 + j < a.b_rows) {
-          const int y = WGRAD ? first : static_cast<int>(out_row), z = WGRAD ? tile.g : 0;
+        } else if (lane == 0 && tile.n0 + j < tile.cols) {
+          const int y = KIND == WGRAD ? first : static_cast<int>(out_row), z = KIND == WGRAD ? tile.g : 0;
           if (tile.add) tma_add_3d(&maps.out, patch, tile.n0 + j, y, z);
           else tma_store_3d(&maps.out, patch, tile.n0 + j, y, z);
         }
@@ -582,10 +639,10 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
   if (warp == 9) tmem_dealloc<CTAS>(tmem, TMEM_COLS);
 }
 
-template <int CTAS, int BN, bool WGRAD>
+template <int CTAS, int BN, int KIND>
 cudaError_t launch(const GroupedMaps& maps, const GroupedArgs& a, int num_sms,
                    cudaStream_t stream) {
-  auto kernel = mx_grouped_kernel<CTAS, BN, WGRAD>;
+  auto kernel = mx_grouped_kernel<CTAS, BN, KIND>;
   constexpr int smem = Shape<CTAS, BN>::SMEM;
   static_assert(smem <= 227 * 1024, "shared memory of one SM");
   static std::atomic<uint64_t> allowed{0};
@@ -593,11 +650,12 @@ cudaError_t launch(const GroupedMaps& maps, const GroupedArgs& a, int num_sms,
   if (e != cudaSuccess) return e;
   // At most this many tiles, whatever the offsets are.
   constexpr int TILE_M = ROWS * CTAS;
-  const int64_t tiles_n = (a.b_rows + BN - 1) / BN;
-  const int64_t tiles_m =
-      WGRAD ? static_cast<int64_t>(a.groups) * ((a.a_rows + TILE_M - 1) / TILE_M)
-            : a.limit / TILE_M + (a.groups < a.limit ? a.groups : a.limit);
-  const int64_t tiles = tiles_m * tiles_n, most = num_sms / CTAS;
+  auto split = [&](int tile) { return a.limit / tile + (a.groups < a.limit ? a.groups : a.limit); };
+  auto whole = [](int64_t n, int tile) { return (n + tile - 1) / tile; };
+  const int64_t tiles = KIND == FORWARD ? split(TILE_M) * whole(a.b_rows, BN)
+                        : KIND == FEW   ? split(BN) * whole(a.a_rows, TILE_M)
+                                        : a.groups * whole(a.a_rows, TILE_M) * whole(a.b_rows, BN);
+  const int64_t most = num_sms / CTAS;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles < most ? tiles : most) * CTAS);
   cfg.blockDim = dim3(THREADS);
@@ -613,12 +671,12 @@ cudaError_t launch(const GroupedMaps& maps, const GroupedArgs& a, int num_sms,
   return cudaLaunchKernelEx(&cfg, kernel, maps, a);
 }
 
-template <bool WGRAD>
+template <int KIND>
 cudaError_t launch_plan(GroupedPlan plan, const GroupedMaps& maps, const GroupedArgs& a,
                         int num_sms, cudaStream_t stream) {
-  if (plan.ctas == 2) return launch<2, 256, WGRAD>(maps, a, num_sms, stream);
-  return plan.cols == 256 ? launch<1, 256, WGRAD>(maps, a, num_sms, stream)
-                          : launch<1, 128, WGRAD>(maps, a, num_sms, stream);
+  if (plan.ctas == 2) return launch<2, 256, KIND>(maps, a, num_sms, stream);
+  return plan.cols == 256 ? launch<1, 256, KIND>(maps, a, num_sms, stream)
+                          : launch<1, 128, KIND>(maps, a, num_sms, stream);
 }
 
 }  // namespace
@@ -630,16 +688,19 @@ cudaError_t launch_plan(GroupedPlan plan, const GroupedMaps& maps, const Grouped
 // keep it busy: weight gradients of 64 experts x 1408 x 2048 from 128 rows each
 // 147 us, 166 in 256 columns, 200 in pairs.  Few tiles: 128 columns, twice as
 // many CTAs.
-GroupedPlan grouped_plan(int64_t rows, int64_t cols, int64_t depth, int groups, int num_sms) {
+GroupedPlan grouped_plan(int64_t rows, int64_t cols, int64_t depth, int groups, bool wgrad,
+                         int num_sms) {
+  if (!wgrad && rows <= static_cast<int64_t>(groups) * FEW_ROWS) return {1, 32, true};
   const int64_t tiles = (rows / ROWS + groups) * ((cols + 255) / 256);
-  if (tiles < 2 * num_sms || depth <= 4 * STEP_K) return {1, 128};
-  return {rows >= static_cast<int64_t>(groups) * 2 * ROWS ? 2 : 1, 256};
+  if (tiles < 2 * num_sms || depth <= 4 * STEP_K) return {1, 128, false};
+  return {rows >= static_cast<int64_t>(groups) * 2 * ROWS ? 2 : 1, 256, false};
 }
 
 cudaError_t launch_grouped(const GroupedMaps& maps, const GroupedArgs& a, bool wgrad,
                            GroupedPlan plan, int num_sms, cudaStream_t stream) {
-  return wgrad ? launch_plan<true>(plan, maps, a, num_sms, stream)
-               : launch_plan<false>(plan, maps, a, num_sms, stream);
+  if (plan.few) return launch<1, 32, FEW>(maps, a, num_sms, stream);
+  return wgrad ? launch_plan<WGRAD>(plan, maps, a, num_sms, stream)
+               : launch_plan<FORWARD>(plan, maps, a, num_sms, stream);
 }
 
 }  // namespace mxq

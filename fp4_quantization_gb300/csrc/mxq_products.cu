@@ -17,13 +17,13 @@ constexpr int64_t kMost = int64_t(1) << 30;
 // E4M3 codes [groups][rows][depth] (depth contiguous): box of one swizzle row
 // of 128 codes x box_rows rows.
 mxq_status encode_codes(CUtensorMap* map, const uint8_t* q, int64_t groups, int64_t rows,
-                        int64_t depth, int box_rows, int rank) {
+                        int64_t depth, int box_rows) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(depth), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(groups)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(depth),
                                  static_cast<cuuint64_t>(depth * rows)};
   const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 1};
-  return mxq::encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, q, dims, strides, box,
+  return mxq::encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, q, dims, strides, box,
                          CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
@@ -78,18 +78,20 @@ mxq_status mx_grouped_gemm(const uint8_t* x_q, const uint8_t* x_s, const uint8_t
   a.offsets = offsets;
   a.groups = static_cast<int>(E);
   a.limit = static_cast<int>(M);
-  a.b_rows = static_cast<int>(N);
   a.depth = static_cast<int>(K);
-  a.a_s = x_s;
-  a.b_s = w_s;
   a.s_ld = K / 32;
   a.dev_err = dev_err;
   a.timeout_ns = mxq::PRODUCT_TIMEOUT_NS;
-  const mxq::GroupedPlan plan = mxq::grouped_plan(M, N, K, a.groups, sms);
+  const mxq::GroupedPlan plan = mxq::grouped_plan(M, N, K, a.groups, false, sms);
+  (plan.few ? a.a_rows : a.b_rows) = static_cast<int>(N);
+  a.a_s = plan.few ? w_s : x_s;
+  a.b_s = plan.few ? x_s : w_s;
   if (K > 0) {
-    st = encode_codes(&maps.a, x_q, 1, M, K, 128, 2);
+    st = encode_codes(plan.few ? &maps.b : &maps.a, x_q, 1, M, K,
+                      plan.few ? plan.box_rows() : 128);
     if (st != MXQ_OK) return st;
-    st = encode_codes(&maps.b, w_q, E, N, K, plan.box_rows(), 3);
+    st = encode_codes(plan.few ? &maps.a : &maps.b, w_q, E, N, K,
+                      plan.few ? 128 : plan.box_rows());
     if (st != MXQ_OK) return st;
   }
   return from_cuda(mxq::launch_grouped(maps, a, false, plan, sms, stream));
@@ -127,11 +129,11 @@ mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, const uint8_
   a.s_ld = M / 32;
   a.dev_err = dev_err;
   a.timeout_ns = mxq::PRODUCT_TIMEOUT_NS;
-  const mxq::GroupedPlan plan = mxq::grouped_plan(N * E, K, M / E, a.groups, sms);
+  const mxq::GroupedPlan plan = mxq::grouped_plan(N * E, K, M / E, a.groups, true, sms);
   if (M > 0) {
-    st = encode_codes(&maps.a, g_q, 1, N, M, 128, 2);
+    st = encode_codes(&maps.a, g_q, 1, N, M, 128);
     if (st != MXQ_OK) return st;
-    st = encode_codes(&maps.b, x_q, 1, K, M, plan.box_rows(), 3);
+    st = encode_codes(&maps.b, x_q, 1, K, M, plan.box_rows());
     if (st != MXQ_OK) return st;
   }
   return from_cuda(mxq::launch_grouped(maps, a, true, plan, sms, stream));

@@ -18,14 +18,15 @@ constexpr uint64_t PRODUCT_TIMEOUT_NS = 1000000000ull;   // 1 s per wait
 // One grouped product: tiles of out = A B^T, where A's and B's rows are codes
 // along the contraction axis.  Forward: A is [limit][depth], B is
 // [groups][b_rows][depth], and group g owns A's (and out's) rows
-// [offsets[g], offsets[g + 1]).  Weight gradient (wgrad != 0): A is
-// [a_rows][limit], B is [b_rows][limit], and group g owns the contraction
-// range [offsets[g], offsets[g + 1]) and the output matrix g.
+// [offsets[g], offsets[g + 1]).  With few rows (GroupedPlan::few) the same with
+// A and B exchanged: A is [groups][a_rows][depth], B is [limit][depth].  Weight
+// gradient: A is [a_rows][limit], B is [b_rows][limit], and group g owns the
+// contraction range [offsets[g], offsets[g + 1]) and the output matrix g.
 struct GroupedArgs {
   const int32_t* offsets;   // [groups + 1], device
   int groups;
   int limit;                // M: no offset is above it
-  int a_rows;               // wgrad: N
+  int a_rows;               // wgrad, few: N
   int b_rows;               // forward: N; wgrad: K
   int depth;                // forward: K
   const uint8_t* a_s;       // E8M0 scales, s_ld bytes a row
@@ -40,8 +41,9 @@ struct GroupedArgs {
 };
 
 struct GroupedMaps {
-  CUtensorMap a;            // 2-D codes, box 128 bytes x 128 rows, 128-byte swizzle
-  CUtensorMap b;            // 3-D codes (depth, row, group), box 128 bytes x GroupedPlan::box_rows() x 1
+  CUtensorMap a;            // 3-D codes (depth, row, group), box 128 bytes x 128 rows x 1, 128-byte
+                            // swizzle
+  CUtensorMap b;            // the same, box 128 bytes x GroupedPlan::box_rows() x 1
   CUtensorMap out;          // 3-D output (column, row, group), box 128 bytes x 32 rows x 1, 128-byte
                             // swizzle; unset unless GroupedArgs::out_vec
 };
@@ -51,12 +53,14 @@ struct GroupedMaps {
 struct GroupedPlan {
   int ctas;
   int cols;
+  bool few;                // few rows a group: they are B, and the weight A
   int box_rows() const { return cols / ctas; }   // rows of one copy of B
 };
 
 // The plan for groups of rows / groups output rows on average, whose elements
 // are sums of `depth` products.
-GroupedPlan grouped_plan(int64_t rows, int64_t cols, int64_t depth, int groups, int num_sms);
+GroupedPlan grouped_plan(int64_t rows, int64_t cols, int64_t depth, int groups, bool wgrad,
+                         int num_sms);
 cudaError_t launch_grouped(const GroupedMaps& maps, const GroupedArgs& a, bool wgrad,
                            GroupedPlan plan, int num_sms, cudaStream_t stream);
 

@@ -100,6 +100,9 @@ GEMM = [
     ("outside_rows", [5, 300], 130, 544, 7, 200),
     ("long_k", [40, 200], 72, 8192 + 32, 0, 0),
     ("ranges", [33, 130], 160, 3 * 8192 - 64, 0, 0),
+    ("few", [100, 0, 3, 1, 0], 300, 1056, 4, 9),
+    ("few_ranges", [5, 40, 0], 203, 2 * 8192 + 96, 0, 0),
+    ("few_wide", [(i * 5) % 9 for i in range(40)], 2500, 512, 0, 0),
     ("chunk_edges", [128, 256, 384], 384, 512, 0, 0),
     ("many_tiles", [700, 90, 2000, 1310], 1400, 736, 0, 0),
     ("many_groups", [(i * 37) % 23 for i in range(300)], 48, 224, 0, 0),
