@@ -681,19 +681,31 @@ cudaError_t launch_plan(GroupedPlan plan, const GroupedMaps& maps, const Grouped
 
 }  // namespace
 
-// Pairs read the fewest bytes of codes a product, and win wherever they fill the
-// GPU with tiles of which most rows are real: gemm 16384 x 14336 x 4096 over 8
-// experts 680 us, 732 in tiles of one CTA.  A short contraction leaves the
+// The cut with the least estimated time: waves of tiles over the GPU, each so
+// many clocks a stage and so many more, as measured with all SMs at work (128
+// columns 500 and 3000, 256 columns 750 and 5500, pairs of CTAs 660 and 5500).
+// Pairs read the fewest bytes of codes a product and win large calls (gemm 16384
+// x 14336 x 4096 over 8 experts 680 us, 732 in 256 columns, 912 in 128), the
+// others where fewer tiles fill the GPU worse (4096 x 2048 x 2048 over 8 experts
+// 26.6, 22.8 and 26.5 us).  A contraction of four stages or less leaves the
 // epilogue alone to bound the call, and two whole accumulators of 128 columns
-// keep it busy: weight gradients of 64 experts x 1408 x 2048 from 128 rows each
-// 147 us, 166 in 256 columns, 200 in pairs.  Few tiles: 128 columns, twice as
-// many CTAs.
+// keep it busiest (weight gradients of 64 experts x 1408 x 2048 from 128 rows
+// each 200, 166 and 147 us).
 GroupedPlan grouped_plan(int64_t rows, int64_t cols, int64_t depth, int groups, bool wgrad,
                          int num_sms) {
   if (!wgrad && rows <= static_cast<int64_t>(groups) * FEW_ROWS) return {1, 32, true};
-  const int64_t tiles = (rows / ROWS + groups) * ((cols + 255) / 256);
-  if (tiles < 2 * num_sms || depth <= 4 * STEP_K) return {1, 128, false};
-  return {rows >= static_cast<int64_t>(groups) * 2 * ROWS ? 2 : 1, 256, false};
+  if (depth <= 4 * STEP_K) return {1, 128, false};
+  auto clocks = [&](int ctas, int bn, int stage, int fixed) {
+    const int64_t tile = ROWS * ctas;
+    const int64_t tiles_m = wgrad ? groups * ((rows / groups + tile - 1) / tile)
+                                  : rows / tile + (groups + 1) / 2;
+    const int64_t tiles = tiles_m * ((cols + bn - 1) / bn), at_once = num_sms / ctas;
+    return (tiles + at_once - 1) / at_once * ((depth + STEP_K - 1) / STEP_K * stage + fixed);
+  };
+  const int64_t narrow = clocks(1, 128, 500, 3000), wide = clocks(1, 256, 750, 5500),
+                pair = clocks(2, 256, 660, 5500);
+  if (narrow <= wide && narrow <= pair) return {1, 128, false};
+  return {pair <= wide ? 2 : 1, 256, false};
 }
 
 cudaError_t launch_grouped(const GroupedMaps& maps, const GroupedArgs& a, bool wgrad,
