@@ -218,24 +218,24 @@ __device__ __forceinline__ void store_patch(const GroupedArgs& a, uint32_t patch
     }
     return;
   }
-  // bf16: a lane a pair of columns that starts on 4 bytes, and in rows that start
-  // on an odd element the first and last column by themselves.
-#pragma unroll 4
+  // bf16: a lane a pair of columns that starts on 4 bytes, and the first or last
+  // column by itself where the row's ends leave it over.
+  uint16_t* p = static_cast<uint16_t*>(a.out) + row * a.ldo + col;
+  const int limit = min(cols, 64), skew = static_cast<int>(a.ldo & 1);
+  const int odd0 = static_cast<int>((reinterpret_cast<uintptr_t>(p) / 2) & 1);
+#pragma unroll 8
   for (int r = 0; r < 32; ++r) {
-    const int64_t first = (row + r) * a.ldo + col;
-    const int odd = static_cast<int>((reinterpret_cast<uintptr_t>(a.out) / 2 + first) & 1);
-    const uint32_t line = patch + r * 128;
-    uint32_t v = lds32(line + (((lane / 4) ^ (r & 7)) << 4) + lane % 4 * 4);
+    const int odd = odd0 ^ (skew & r);
+    const uint32_t v = lds32(patch + r * 128 + (((lane / 4) ^ (r & 7)) << 4) + lane % 4 * 4);
     const uint32_t next = __shfl_down_sync(~0u, v, 1);
-    uint16_t* p = static_cast<uint16_t*>(a.out) + first;
-    if (r >= rows) continue;
-    if (odd && lane == 0 && cols > 0) p[0] = static_cast<uint16_t>(v);
-    if (odd) v = v >> 16 | next << 16;
     const int c = 2 * lane + odd;
-    if (c + 1 < cols && c + 1 < 64)
-      stg32(p + c, v);
-    else if (c < cols && c < 64)
-      p[c] = static_cast<uint16_t>(v);
+    if (r < rows) {
+      if (c + 1 < limit) stg32(p + c, odd ? v >> 16 | next << 16 : v);
+      if (odd && lane == 0 && limit > 0) p[0] = static_cast<uint16_t>(v);
+      if (((limit - odd) & 1) && limit > odd && lane == (limit - 1) / 2)
+        p[limit - 1] = static_cast<uint16_t>(limit & 1 ? v : v >> 16);
+    }
+    p += a.ldo;
   }
 }
 
