@@ -249,7 +249,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
   int load_item = item_first, load_k0 = k_first, load_k = 0, load_row = 0;
   uint32_t scale[DEPTH][2][2] = {};                   // four scales a row, or two and two
   uint32_t phase = 0, used = 0, pending = 0;          // a bit a place
-  bool ok = true;                                     // no wait ran out
+  bool ok = true;                                     // no wait of the warp ran out
   auto load_start = [&] {
     load_k = start_of(load_k0);
     if (load_item >= item_end) return;
@@ -263,14 +263,13 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
   };
   auto load_next = [&](int i, uint32_t (&v)[2][2]) {
     const int k1 = min(load_k0 + room, k_end);
-    if (load_item < item_end && load_k < k1) {
+    if (ok && load_item < item_end && load_k < k1) {
       if (tile == 0) {
         // The place has been read by all the part's warps.
         if (used >> i & 1) {
-          ok = ok && mbar_wait_bounded(empties + 8 * i, ~phase >> i & 1, a.timeout_ns);
-          __syncwarp();
+          ok = __all_sync(~0u, mbar_wait_bounded(empties + 8 * i, ~phase >> i & 1, a.timeout_ns));
         }
-        if (elect_one()) {
+        if (ok && elect_one()) {
           mbar_arrive_expect_tx(fulls + 8 * i, tiles * STEP_BYTES);
           tma_load_2d(ring + i * (tiles * STEP_BYTES), &codes, load_k / 2, load_row, fulls + 8 * i);
         }
@@ -301,9 +300,11 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
     }
   };
   auto wait_for = [&](int i) {
-    ok = ok && mbar_wait_bounded(fulls + 8 * i, phase >> i & 1, a.timeout_ns);
-    phase ^= 1u << i;
-    pending &= ~(1u << i);
+    ok = ok && __all_sync(~0u, mbar_wait_bounded(fulls + 8 * i, phase >> i & 1, a.timeout_ns));
+    if (ok) {
+      phase ^= 1u << i;
+      pending &= ~(1u << i);
+    }
     __syncwarp();
   };
   auto release = [&](int i) {
@@ -558,9 +559,11 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
       staged = -1;
     }
   }
+  // Copies still in flight (after a wait that ran out) land before the memory is
+  // given back.
 #pragma unroll 1
   for (int i = 0; i < DEPTH; ++i)
-    if (pending >> i & 1) wait_for(i);
+    if (pending >> i & 1) mbar_wait_bounded(fulls + 8 * i, phase >> i & 1, a.timeout_ns);
   if (!ok && a.dev_err) atomicOr(a.dev_err, MXQ_DEVERR_TIMEOUT);
 }
 
