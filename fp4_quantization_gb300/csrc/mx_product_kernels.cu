@@ -17,7 +17,7 @@ constexpr int STEP_K = 128;           // contraction bytes of one pipeline stage
 // Stages whose scales are fetched together: 64 bytes a row, by four threads in
 // one request.  The scales are 3% of the bytes, but fetched 16 bytes at a time
 // they were 27% of the requests to L2, and the codes' copies waited for them.
-constexpr int CHUNK = 16;
+constexpr int WINDOW = 16;
 constexpr int THREADS = 320;          // 4 epilogue, 4 scale, 1 copy, 1 issuing warp
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int FEW_ROWS = 32;          // rows of a group on average up to which they are B
@@ -42,8 +42,12 @@ struct Shape {
   static constexpr int A_BYTES = ROWS * STEP_K;
   static constexpr int B_ROWS = BN / CTAS;                          // of each CTA
   static constexpr int STAGE_BYTES = A_BYTES + B_ROWS * STEP_K;
-  static constexpr int STAGES = STAGE_BYTES > 40 * 1024 ? 3 : BN >= 128 ? 4 : 8;
+  static constexpr int STAGES = STAGE_BYTES > 40 * 1024 ? 4 : BN >= 128 ? 5 : 8;
   static constexpr int B_TILES = (BN + 127) / 128;                  // scale tiles of B a stage
+  // Stages whose scales share a place in shared memory: the fewer, the more is
+  // left for codes in flight, which bound large calls (a pair's fifth stage: gemm
+  // 16384 x 14336 x 4096 over 8 experts 686 -> 660 us).
+  static constexpr int CHUNK = STAGE_BYTES > 40 * 1024 ? 4 : 8;
   static constexpr int SCALE_BYTES = CHUNK * 512 * (1 + B_TILES);   // one scale chunk
   static constexpr int SCALE_CHUNKS = 2;
   // Patches of 32 rows x 128 bytes that the epilogue's four warps stage: two
@@ -243,6 +247,7 @@ template <int CTAS, int BN, int KIND>
 __global__ void __launch_bounds__(THREADS, 1)
 mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a) {
   using S = Shape<CTAS, BN>;
+  constexpr int CHUNK = S::CHUNK;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_up_shared<1024>(smem_raw);
   const uint32_t stages = smem_addr(smem);
@@ -445,7 +450,7 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
       while (at >= end) {
         if (!walk.next(a, tile)) return false;
         const int row = tile.m0 + static_cast<int>(rank) * ROWS + r;
-        at = tile.step0() / CHUNK * (CHUNK * 4);
+        at = tile.step0() / WINDOW * (WINDOW * 4);
         end = tile.first < tile.end ? tile.end / 32 : at;
         a_left = tile.rows - row;
         b_left = min(tile.cols - tile.n0, BN) - r;
@@ -467,40 +472,48 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
           else
             load_scales(v[b][i], hi[b][i], p, has, b == 0 ? a_end : b_end);
         }
-      at += CHUNK * 4;
+      at += WINDOW * 4;
       return true;
     };
     uint32_t chunk = 0;
-    for (bool more = load(); more; ++chunk) {
-      const uint32_t c = chunk % S::SCALE_CHUNKS;
-      if (chunk >= S::SCALE_CHUNKS &&
-          !mbar_wait_bounded(sc_empty + 8 * c, (chunk / S::SCALE_CHUNKS - 1) & 1, a.timeout_ns)) {
-        ok = false;
-        break;
-      }
-      const uint32_t dst = scales + c * S::SCALE_BYTES + piece * 2048 + r * 16;
+    while (ok && load()) {
+      const int step = at / 4 - WINDOW;      // of this window's first stage
 #pragma unroll
-      for (int b = 0; b <= S::B_TILES; ++b) {
-        if (!whole) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[b][i] = shift_scales(
-                v[b][i], hi[b][i],
-                static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row_scales(b, i))) & 15);
+      for (int h = 0; h < WINDOW / CHUNK; ++h) {
+        if (step + (h + 1) * CHUNK <= tile.step0() || step + h * CHUNK >= tile.step1()) continue;
+        const uint32_t c = chunk % S::SCALE_CHUNKS;
+        if (chunk >= S::SCALE_CHUNKS &&
+            !mbar_wait_bounded(sc_empty + 8 * c, (chunk / S::SCALE_CHUNKS - 1) & 1, a.timeout_ns)) {
+          ok = false;
+          break;
         }
-        const uint32_t to = dst + b * CHUNK * 512;
-        sts128(to, v[b][0].x, v[b][1].x, v[b][2].x, v[b][3].x);
-        sts128(to + 512, v[b][0].y, v[b][1].y, v[b][2].y, v[b][3].y);
-        sts128(to + 1024, v[b][0].z, v[b][1].z, v[b][2].z, v[b][3].z);
-        sts128(to + 1536, v[b][0].w, v[b][1].w, v[b][2].w, v[b][3].w);
+        ++chunk;
+        constexpr int PIECES = CHUNK / 4;
+        if (piece / PIECES == h) {
+          const uint32_t dst = scales + c * S::SCALE_BYTES + piece % PIECES * 2048 + r * 16;
+#pragma unroll
+          for (int b = 0; b <= S::B_TILES; ++b) {
+            if (!whole) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                v[b][i] = shift_scales(
+                    v[b][i], hi[b][i],
+                    static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row_scales(b, i))) & 15);
+            }
+            const uint32_t to = dst + b * CHUNK * 512;
+            sts128(to, v[b][0].x, v[b][1].x, v[b][2].x, v[b][3].x);
+            sts128(to + 512, v[b][0].y, v[b][1].y, v[b][2].y, v[b][3].y);
+            sts128(to + 1024, v[b][0].z, v[b][1].z, v[b][2].z, v[b][3].z);
+            sts128(to + 1536, v[b][0].w, v[b][1].w, v[b][2].w, v[b][3].w);
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CTAS == 2) mbar_arrive_cluster(cluster_addr(sc_full + 8 * c, 0));
+          else mbar_arrive(sc_full + 8 * c);
+        }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (CTAS == 2) mbar_arrive_cluster(cluster_addr(sc_full + 8 * c, 0));
-        else mbar_arrive(sc_full + 8 * c);
-      }
-      more = load();
     }
   } else {
     // ---- epilogue: warp w reads lanes 32 w .. 32 w + 31, a row each ----
@@ -683,11 +696,11 @@ cudaError_t launch_plan(GroupedPlan plan, const GroupedMaps& maps, const Grouped
 
 // The cut with the least estimated time: waves of tiles over the GPU, each so
 // many clocks a stage and so many more, as measured with all SMs at work (128
-// columns 500 and 3000, 256 columns 750 and 5500, pairs of CTAs 660 and 5500).
+// columns 460 and 2500, 256 columns 720 and 5000, pairs of CTAs 620 and 7000).
 // Pairs read the fewest bytes of codes a product and win large calls (gemm 16384
-// x 14336 x 4096 over 8 experts 680 us, 732 in 256 columns, 912 in 128), the
-// others where fewer tiles fill the GPU worse (4096 x 2048 x 2048 over 8 experts
-// 26.6, 22.8 and 26.5 us).  A contraction of four stages or less leaves the
+// x 14336 x 4096 over 8 experts 657 us, 682 in 256 columns, 856 in 128), the
+// others where its tiles fill the GPU worse (4096 x 2048 x 2048 over 8 experts
+// 25.6, 21.8 and 25.5 us).  A contraction of four stages or less leaves the
 // epilogue alone to bound the call, and two whole accumulators of 128 columns
 // keep it busiest (weight gradients of 64 experts x 1408 x 2048 from 128 rows
 // each 200, 166 and 147 us).
@@ -702,8 +715,8 @@ GroupedPlan grouped_plan(int64_t rows, int64_t cols, int64_t depth, int groups, 
     const int64_t tiles = tiles_m * ((cols + bn - 1) / bn), at_once = num_sms / ctas;
     return (tiles + at_once - 1) / at_once * ((depth + STEP_K - 1) / STEP_K * stage + fixed);
   };
-  const int64_t narrow = clocks(1, 128, 500, 3000), wide = clocks(1, 256, 750, 5500),
-                pair = clocks(2, 256, 660, 5500);
+  const int64_t narrow = clocks(1, 128, 460, 2500), wide = clocks(1, 256, 720, 5000),
+                pair = clocks(2, 256, 620, 7000);
   if (narrow <= wide && narrow <= pair) return {1, 128, false};
   return {pair <= wide ? 2 : 1, 256, false};
 }
