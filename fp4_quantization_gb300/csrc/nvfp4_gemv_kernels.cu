@@ -87,12 +87,15 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
 // warps' load path; its scales are 4 bytes a thread and row.
 //
 // One step: codes at `ws`, the block scales of k = 64 t .. 64 t + 63 of rows g
-// and g + 8 in s, x fragments at xs, 8 pieces of [rows][4] 16-byte units.  Thread
-// (g, t) multiplies weight rows g and g + 8, and row g (and g + 8) of x, at those
-// k; the instruction's k order is the codes' order, on both sides.
+// and g + 8 in s, and row g (and g + 8) of x at those k in 8 pieces of 16 bytes,
+// x_step apart (0, at zeros, where there is no such row).  Thread (g, t)
+// multiplies weight rows g and g + 8 by them; the instruction's k order is the
+// codes' order, on both sides.
 template <int TOKS>
 __device__ __forceinline__ void multiply_step(float (&sum)[Shape<TOKS>::TILES][4], uint32_t ws,
-                                              const uint32_t (&s)[2], uint32_t xs, int rows, int g,
+                                              const uint32_t (&s)[2],
+                                              const uint32_t (&x_at)[Shape<TOKS>::TILES],
+                                              const uint32_t (&x_step)[Shape<TOKS>::TILES], int g,
                                               int t) {
   uint4 c[2][2];
 #pragma unroll
@@ -114,8 +117,7 @@ __device__ __forceinline__ void multiply_step(float (&sum)[Shape<TOKS>::TILES][4
       uint4 x[Shape<TOKS>::TILES];
 #pragma unroll
       for (int m = 0; m < Shape<TOKS>::TILES; ++m) {
-        x[m] = make_uint4(0, 0, 0, 0);
-        if (g + 8 * m < rows) x[m] = lds128(xs + ((p * rows + g + 8 * m) * 4 + t) * 16);
+        x[m] = lds128(x_at[m] + p * x_step[m]);
       }
       uint32_t v[2][4];
 #pragma unroll
@@ -161,6 +163,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
   __shared__ int list[TOKS + 2];                          // rows of the expert, their number, the next
   __shared__ int best_of[TILES * WARPS];
   __shared__ uint64_t full[WARPS][DEPTH], empty[WARPS][DEPTH];   // of a part's places
+  __shared__ uint4 zeros[1];
   __shared__ float2 unit[TOKS];                           // what a sum of staged row i is multiplied by
   const int tid = threadIdx.x, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int warp = __shfl_sync(~0u, tid / 32, 0);          // the same for the warp, known to be
@@ -243,11 +246,12 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
     }
     fence_barrier_init();
   }
+  if (tid == 0) zeros[0] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   const bool words = a.k % 64 == 0;                   // rows of scales start on 4 bytes
   const uint8_t* s[2] = {};                           // this thread's scales at k = 0
   int load_item = item_first, load_k0 = k_first, load_k = 0, load_row = 0;
-  uint32_t scale[DEPTH][2][2] = {};                   // four scales a row, or two and two
+  uint32_t scale[DEPTH][2][2] = {};                   // four scales a row, or two and two apart
   uint32_t phase = 0, used = 0, pending = 0;          // a bit a place
   bool ok = true;                                     // no wait of the warp ran out
   auto load_start = [&] {
@@ -276,16 +280,20 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
       }
       used |= 1u << i;
       pending |= 1u << i;
-      const int left = a.k - load_k - 64 * t;
+      if (words && load_k + STEP_K <= a.k) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint8_t* p = s[h] + load_k / 16;
-        if (words && left >= 64) {
-          v[h][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-        } else {
-          const uint16_t* two = reinterpret_cast<const uint16_t*>(p);
-          v[h][0] = left > 0 ? __ldg(two) : 0;
-          v[h][1] = left > 32 ? __ldg(two + 1) : 0;
+        for (int h = 0; h < 2; ++h) {
+          v[h][0] = __ldg(reinterpret_cast<const uint32_t*>(s[h] + load_k / 16));
+          v[h][1] = 0;
+        }
+      } else {
+        const int left = a.k - load_k - 64 * t;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint16_t* p = reinterpret_cast<const uint16_t*>(s[h] + load_k / 16);
+          const uint32_t lo = left > 0 ? __ldg(p) : 0, hi = left > 32 ? __ldg(p + 1) : 0;
+          v[h][0] = lo;
+          v[h][1] = hi;
         }
       }
     }
@@ -509,6 +517,14 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
             load_start();
           }
           int k = start_of(k0);
+          // This thread's pieces of x at k = k0.
+          uint32_t x_first[TILES], x_step[TILES];
+#pragma unroll
+          for (int m = 0; m < TILES; ++m) {
+            const bool has = g + 8 * m < rows;
+            x_first[m] = has ? xs + ((g + 8 * m) * 4 + t) * 16 : smem_addr(zeros);
+            x_step[m] = has ? rows * 64 : 0;
+          }
           bool filled = false;
           do {
             filled = fill;
@@ -516,10 +532,13 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
             for (int i = 0; i < DEPTH; ++i) {
               if (!fill && k < k1) {
                 wait_for(i);
-                const uint32_t four[2] = {words ? scale[i][0][0] : scale[i][0][0] | scale[i][0][1] << 16,
-                                          words ? scale[i][1][0] : scale[i][1][0] | scale[i][1][1] << 16};
-                multiply_step<TOKS>(sum, ring + (i * tiles + tile) * STEP_BYTES, four,
-                                    xs + (k - k0) * rows * 2, rows, g, t);
+                const uint32_t four[2] = {scale[i][0][0] | scale[i][0][1] << 16,
+                                          scale[i][1][0] | scale[i][1][1] << 16};
+                uint32_t x_at[TILES];
+#pragma unroll
+                for (int m = 0; m < TILES; ++m) x_at[m] = x_first[m] + (k - k0) / 32 * x_step[m];
+                multiply_step<TOKS>(sum, ring + (i * tiles + tile) * STEP_BYTES, four, x_at, x_step,
+                                    g, t);
                 release(i);
               }
               load_next(i, scale[i]);
