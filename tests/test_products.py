@@ -100,6 +100,7 @@ GEMM = [
     ("outside_rows", [5, 300], 130, 544, 7, 200),
     ("long_k", [40, 200], 72, 8192 + 32, 0, 0),
     ("ranges", [33, 130], 160, 3 * 8192 - 64, 0, 0),
+    ("ranges_odd", [130, 200], 161, 8192 + 64, 0, 0),
     ("few", [100, 0, 3, 1, 0], 300, 1056, 4, 9),
     ("few_ranges", [5, 40, 0], 203, 2 * 8192 + 96, 0, 0),
     ("few_wide", [(i * 5) % 9 for i in range(40)], 2500, 512, 0, 0),
@@ -194,6 +195,63 @@ def test_grouped_gemm_scale_extremes():
     assert torch.equal(y[0, ::8], want[0]) and y[1, 8] == want[1, 1] and y[1, 0] == 0
 
 
+@gpu
+@pytest.mark.parametrize("sizes,N,K", [([40, 3, 200], 300, 416), ([9, 2, 0, 5], 200, 96)],
+                         ids=["forward", "few"])
+def test_grouped_gemm_keeps_nan_where_it_is(sizes, N, K):
+    """A NaN code in a row of x reaches that row alone, a NaN scale (255) of a
+    weight row that column of its expert alone, and neither other groups'
+    rows in the same tile."""
+    gen = generator(15)
+    M, E = sum(sizes), len(sizes)
+    x_q, x_s = mx_operand(gen, True, M, K)
+    w_q, w_s = mx_operand(gen, True, E, N, K)
+    off = offsets_of(sizes)
+    row, e, col = sizes[0], 0, N - 1            # the second group's first row
+    x_q[row, K - 1] = 0x7F
+    w_s[e, col, 0] = 255
+    y = mxq.mx_grouped_gemm(x_q, x_s, w_q, w_s, off, out_dtype=torch.float32)
+    bad = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    bad[row], bad[:sizes[0], col] = True, True
+    assert torch.equal(y.isnan(), bad)
+
+
+@gpu
+@pytest.mark.slow
+def test_products_past_2_31_elements():
+    """Outputs and operands whose element numbers pass 32 bits: the last rows,
+    experts and columns against the definition."""
+    gen = generator(16)
+    M, N, K, E = 70016, 32768, 32, 3
+    x_q, x_s = mx_operand(gen, True, M, K)
+    w_q, w_s = mx_operand(gen, True, E, N, K)
+    off = offsets_of([100, 34900, M - 35000])
+    y = mxq.mx_grouped_gemm(x_q, x_s, w_q, w_s, off)
+    for rows, e in ((slice(0, 70), 0), (slice(34990, 35000), 1), (slice(M - 130, M), 2)):
+        want = mx_values(x_q[rows], x_s[rows]) @ mx_values(w_q[e], w_s[e]).t()
+        check(y[rows], want, None, True)
+    del y
+    E, N, K, M = 40, 8192, 8192, 1280
+    g_q, g_s = mx_operand(gen, True, N, M)
+    x_q, x_s = mx_operand(gen, True, K, M)
+    off = offsets_of([32] * E)
+    dw = mxq.mx_grouped_wgrad(g_q, g_s, x_q, x_s, off, out_dtype=torch.bfloat16)
+    for e in (0, 31, E - 1):
+        a = slice(32 * e, 32 * e + 32)
+        want = mx_values(g_q[-300:, a], g_s[-300:, e:e + 1]) @ mx_values(x_q[:, a], x_s[:, e:e + 1]).t()
+        check(dw[e, -300:], want, None, True)
+    del dw
+    E, N, K = 72, 16384, 8192
+    q = torch.randint(0, 256, (E, N, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    s = pick(gen, [0x30, 0x38, 0x40], E, N, K // 16)
+    g = torch.ones(E, device="cuda")
+    x = nv_rows(gen, True, 2, K)
+    ids = torch.tensor([E - 1, 0], dtype=torch.int32, device="cuda")
+    y = mxq.nvfp4_gemv(x, q, s, g, experts=ids, out_dtype=torch.float32)
+    for r, e in enumerate(ids.tolist()):
+        check(y[r, -500:], nv_values(q[e, -500:], s[e, -500:]) @ x[r].double(), None, True)
+
+
 # ---------------------------------------------------------------------------
 # mx_grouped_wgrad
 # ---------------------------------------------------------------------------
@@ -234,6 +292,24 @@ def test_grouped_wgrad(name, sizes, N, K, before, after, dtype, exact):
         a, b = int(off[e]), int(off[e + 1])
         check(dw[e], g[:, a:b] @ x[:, a:b].t(),
               rows * 2.0 ** -23 * (g[:, a:b].abs() @ x[:, a:b].abs().t()), exact, f"{name} {e}")
+
+
+@gpu
+def test_grouped_wgrad_keeps_nan_where_it_is():
+    """NaN codes and scales in the 32 rows after a group's end, which share a
+    128-row stage with it, stay out of its gradient."""
+    gen = generator(17)
+    sizes, N, K = [96, 32, 160], 136, 80
+    M, off = sum(sizes), offsets_of(sizes)
+    g_q, g_s = mx_operand(gen, True, N, M)
+    x_q, x_s = mx_operand(gen, True, K, M)
+    g_q[:, 96:128] = 0x7F
+    x_s[:, 3] = 255
+    dw = mxq.mx_grouped_wgrad(g_q, g_s, x_q, x_s, off)
+    assert dw[1].isnan().all()
+    g, x = mx_values(g_q, g_s), mx_values(x_q, x_s)
+    for e, (a, b) in ((0, (0, 96)), (2, (128, 288))):
+        check(dw[e], g[:, a:b] @ x[:, a:b].t(), None, True)
 
 
 @gpu
@@ -408,6 +484,23 @@ def test_gemv_strides_and_quantizer():
     want, bound = gemv_reference(x, nv["q_row"][None], nv["s_row"][None], nv["global_scale"], None, 1)
     check(out[:, 5:5 + N], want, bound, False)
     assert (out[:, :5] == 3).all() and (out[:, 5 + N:] == 3).all()
+
+
+@gpu
+def test_gemv_infinities_and_nan():
+    """An infinity in a row of x gives what 64 bits give, and a NaN scale its
+    column alone; neither reaches other rows."""
+    gen = generator(18)
+    T, N, K = 4, 40, 320
+    q, s, g = nv_operand(gen, True, 1, N, K)
+    x = nv_rows(gen, True, T, K)
+    s[0, 7, 3] = 0x7F
+    x[1, 100], x[2, 5] = float("inf"), float("nan")
+    y = mxq.nvfp4_gemv(x, q[0], s[0], g, out_dtype=torch.float32).double()
+    want = (x.double().unsqueeze(1) * nv_values(q, s)).sum(-1) * g.double()
+    assert torch.equal(y.isnan(), want.isnan())
+    here = ~want.isnan()
+    assert torch.equal(y[here], want[here])
 
 
 @gpu
