@@ -64,10 +64,9 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t pair) {
   return h;
 }
 
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 b) {
+  const __half2 d = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
+  return *reinterpret_cast<const uint32_t*>(&d);
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -92,7 +91,7 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
 // multiplies weight rows g and g + 8 by them; the instruction's k order is the
 // codes' order, on both sides.
 template <int TOKS>
-__device__ __forceinline__ void multiply_step(float (&sum)[Shape<TOKS>::TILES][4], uint32_t ws,
+__device__ __forceinline__ void multiply_step(float (&acc)[2][Shape<TOKS>::TILES][4], uint32_t ws,
                                               const uint32_t (&s)[2],
                                               const uint32_t (&x_at)[Shape<TOKS>::TILES],
                                               const uint32_t (&x_step)[Shape<TOKS>::TILES], int g,
@@ -103,14 +102,14 @@ __device__ __forceinline__ void multiply_step(float (&sum)[Shape<TOKS>::TILES][4
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       c[h][i] = lds128(ws + (g + 8 * h) * 128 + (((2 * t + i) ^ g) << 4));
-  float acc[2][Shape<TOKS>::TILES][4] = {};
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
-    uint32_t sc[2];
+    __half2 sc[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t pair = e4m3x2_to_f16(b < 2 ? s[h] & 0xFFFF : s[h] >> 16);
-      sc[h] = prmt(pair, pair, b % 2 ? 0x3232 : 0x1010);
+      const __half2 two = *reinterpret_cast<const __half2*>(&pair);
+      sc[h] = b % 2 ? __high2half2(two) : __low2half2(two);
     }
 #pragma unroll
     for (int p = 2 * b; p < 2 * b + 2; ++p) {
@@ -133,11 +132,6 @@ __device__ __forceinline__ void multiply_step(float (&sum)[Shape<TOKS>::TILES][4
       }
     }
   }
-  // Sums of 128 terms at a time: the instruction cuts its sums off.
-#pragma unroll
-  for (int m = 0; m < Shape<TOKS>::TILES; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum[m][i] += acc[0][m][i] + acc[1][m][i];
 }
 
 // Persistent CTAs (clusters of them) take an equal share each of the items
@@ -528,6 +522,8 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
           bool filled = false;
           do {
             filled = fill;
+            // Sums of at most 512 terms at a time: the instruction cuts its sums off.
+            float acc[2][TILES][4] = {};
 #pragma unroll
             for (int i = 0; i < DEPTH; ++i) {
               if (!fill && k < k1) {
@@ -537,13 +533,17 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
                 uint32_t x_at[TILES];
 #pragma unroll
                 for (int m = 0; m < TILES; ++m) x_at[m] = x_first[m] + (k - k0) / 32 * x_step[m];
-                multiply_step<TOKS>(sum, ring + (i * tiles + tile) * STEP_BYTES, four, x_at, x_step,
+                multiply_step<TOKS>(acc, ring + (i * tiles + tile) * STEP_BYTES, four, x_at, x_step,
                                     g, t);
                 release(i);
               }
               load_next(i, scale[i]);
               if (!fill) k += turn;
             }
+#pragma unroll
+            for (int m = 0; m < TILES; ++m)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sum[m][i] += acc[0][m][i] + acc[1][m][i];
             fill = false;
           } while (filled || k < k1);
           held_item = k0 + room < k_end ? item : item + 1;     // what the loads have begun
