@@ -357,7 +357,8 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
   auto stage = [&](int rows, int k0, int k1, float global, int (&below)[TILES]) {
     const int all = (k1 - k0 + STEP_K - 1) / STEP_K * (STEP_K / 8);
     const int per = rows <= 1 ? 8 : rows <= 2 ? 4 : rows <= 4 ? 2 : 1;   // warps a row
-    const int p0 = (warp % per) * 32 + lane;
+    // A warp's 32 pieces in an order that spreads its stores over the banks.
+    const int p0 = (warp % per) * 32 + lane % 4 * 8 + lane / 4;
     // Piece p is k = 8 p: of its 256, thread (p / 8) % 4's piece p % 8.
     auto place = [&](int m, int p) {
       return xs + (((p / 32 * 8 + p % 8) * rows + m) * 4 + p / 8 % 4) * 16;
@@ -601,7 +602,7 @@ struct Plan {
 Plan choose(const GemvArgs& a, int rows, int toks, int x_bytes, int64_t slots, int num_sms) {
   const int64_t steps = (a.k + STEP_K - 1) / STEP_K;
   auto items = [&](int tiles) { return (a.n + tiles * 16 - 1) / (tiles * 16) * slots; };
-  Plan plan{WARPS, 1, toks};
+  Plan plan{WARPS, 1, a.experts || a.rows > toks ? toks : a.rows};
   const int64_t want = num_sms * 3 / 2;
   while (rows <= 2 && plan.tiles > 1 && items(plan.tiles) < want) plan.tiles /= 2;
   while (plan.cluster < 8 && items(plan.tiles) * plan.cluster < want &&
@@ -611,7 +612,7 @@ Plan choose(const GemvArgs& a, int rows, int toks, int x_bytes, int64_t slots, i
   // Rows whose range of K is staged whole, if that takes all that are expected.
   const int64_t range = (steps + plan.cluster - 1) / plan.cluster;
   const int64_t fit = x_bytes / (2 * STEP_K) / (range > 0 ? range : 1);
-  if (fit >= rows && fit < toks) plan.cap = static_cast<int>(fit);
+  if (fit >= rows && fit < plan.cap) plan.cap = static_cast<int>(fit);
   return plan;
 }
 
