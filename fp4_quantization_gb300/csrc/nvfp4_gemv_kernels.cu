@@ -442,13 +442,15 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
       const int n = rows == 1 ? pair : pair / rows, at = item_at(first + n).n0 + col;
       if (at < a.n) store_out(a, row_at(pair - n * rows), at, v);
     };
+    if (cluster == 1 || parts > 1) {
 #pragma unroll 1
-    for (int pair = tid / width; pair < count * rows; pair += step) {
-      float v = 0;
+      for (int pair = tid / width; pair < count * rows; pair += step) {
+        float v = 0;
 #pragma unroll 1
-      for (int p = 0; p < parts; ++p) v += *place(pair, p);
-      if (cluster == 1) write(pair, v);
-      else *place(pair, 0) = v;             // this thread's own
+        for (int p = 0; p < parts; ++p) v += *place(pair, p);
+        if (cluster == 1) write(pair, v);
+        else *place(pair, 0) = v;           // this thread's own
+      }
     }
     if (cluster == 1) {
       __syncthreads();
@@ -458,10 +460,12 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
 #pragma unroll 1
     for (int pair = tid / width * cluster + rank; pair < count * rows; pair += step * cluster) {
       const uint32_t at = smem_addr(place(pair, 0));
-      float v = 0;
+      float from[8], v = 0;
+#pragma unroll
+      for (int p = 0; p < 8; ++p) from[p] = p < cluster ? ld_cluster_f32(at, p) : 0.f;
 #pragma unroll
       for (int p = 0; p < 8; ++p)
-        if (p < cluster) v += ld_cluster_f32(at, p);
+        if (p < cluster) v += from[p];
       write(pair, v);
     }
     cluster_sync();
