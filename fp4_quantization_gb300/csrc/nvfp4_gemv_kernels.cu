@@ -26,6 +26,7 @@ constexpr int WARPS = 8;
 constexpr int STEP_K = 256;          // K of one step of a warp: a line of codes a row
 constexpr int STEP_BYTES = 16 * STEP_K / 2;
 constexpr int SUM_BYTES = 8 * 1024;  // partial sums of some items
+constexpr int BATCH = 4;             // 16-byte loads of x in flight a thread
 
 // Rows of x at a time: up to 8 or 16.  Two CTAs share an SM.
 template <int TOKS>
@@ -67,6 +68,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t pair) {
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 b) {
   const __half2 d = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
   return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// A pair of bf16 values, each 0 unless its magnitude's bits are in [low, lim).
+__device__ __forceinline__ uint32_t in_window(uint32_t pair, uint32_t low, uint32_t lim) {
+  const uint32_t lo = pair & 0x7FFF, hi = (pair >> 16) & 0x7FFF;
+  return (lo >= low && lo < lim ? pair & 0xFFFF : 0) |
+         (hi >= low && hi < lim ? pair & 0xFFFF0000 : 0);
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -155,7 +163,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
   __shared__ uint16_t active[GEMV_EXPERTS_MAX];           // the experts that have rows
   __shared__ int warp_sum[WARPS];
   __shared__ int list[TOKS + 2];                          // rows of the expert, their number, the next
-  __shared__ int best_of[TILES * WARPS];
+  __shared__ uint32_t extent[TILES * WARPS];               // of a warp's share of a row of x
   __shared__ uint64_t full[WARPS][DEPTH], empty[WARPS][DEPTH];   // of a part's places
   __shared__ uint4 zeros[1];
   __shared__ float2 unit[TOKS];                           // what a sum of staged row i is multiplied by
@@ -373,20 +381,35 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
       const int row = row_at(m);
       const uint4* x = reinterpret_cast<const uint4*>(
           a.x + static_cast<int64_t>(a.share == 1 ? row : row / a.share) * a.ldx + k0);
-      uint32_t best = 0;
-#pragma unroll 4
-      for (int p = p0; p < all; p += per * 32) {
-        const uint4 v = 8 * p < k1 - k0 ? __ldg(x + p) : make_uint4(0, 0, 0, 0);
-        sts128(place(m, p), v.x, v.y, v.z, v.w);
+      // The largest magnitude, and 0x7FFF + m for the smallest m > 0 (so that 0
+      // is the largest of these as signed numbers), a pair of each.
+      uint32_t most = 0, least = 0x7FFF7FFF;
+#pragma unroll 1
+      for (int p = p0; p < all; p += BATCH * per * 32) {
+        uint4 v[BATCH];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t lo = word(v, j) & 0x7FFF, hi = (word(v, j) >> 16) & 0x7FFF;
-          if (lo < lim) best = max(best, lo);
-          if (hi < lim) best = max(best, hi);
+        for (int b = 0; b < BATCH; ++b) {
+          const int at = p + b * per * 32;
+          v[b] = 8 * at < k1 - k0 ? __ldg(x + at) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+          const int at = p + b * per * 32;
+          if (at >= all) break;
+          sts128(place(m, at), v[b].x, v[b].y, v[b].z, v[b].w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t mag = word(v[b], j) & 0x7FFF7FFF;
+            if (below[i] < 256) mag = in_window(mag, 0, lim);
+            most = __vmaxu2(most, mag);
+            least = __vmins2(least, mag + 0x7FFF7FFF);
+          }
         }
       }
-      best = __reduce_max_sync(~0u, best);
-      if (lane == 0) best_of[i * WARPS + warp] = static_cast<int>(best);
+      most = __reduce_max_sync(~0u, max(most & 0xFFFF, most >> 16));
+      least ^= 0x80008000;                 // m - 1, or 0xFFFF
+      least = __reduce_min_sync(~0u, min(least & 0xFFFF, least >> 16));
+      if (lane == 0) extent[i * WARPS + warp] = least << 16 | most;
     }
     __syncthreads();
     bool left = false;
@@ -395,8 +418,9 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
       const int m = warp / per + i * WARPS;
       if (m >= rows) break;
       const uint32_t lim = below[i] << 7;
-      int most = lane < per ? best_of[i * WARPS + warp / per * per + lane] : 0;
-      most = __reduce_max_sync(~0u, most);
+      const uint32_t own = lane < per ? extent[i * WARPS + warp / per * per + lane] : 0xFFFF0000;
+      const uint32_t least = __reduce_min_sync(~0u, own >> 16);
+      const int most = static_cast<int>(__reduce_max_sync(~0u, own & 0xFFFF));
       const int high = most >> 7;
       if (lane == 0) {                     // the same from each of the row's warps
         // G_e over the rows' factor; both in one step and the powers of two apart,
@@ -410,18 +434,23 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
       }
       const uint32_t low = max(high - 28, 0) << 7;
       const float up = __uint_as_float(static_cast<uint32_t>(min(141 - high, 127) + 127) << 23);
+      const bool some = least + 1 < low;   // smaller ones than the window's
+      left |= some;
+      const bool whole_row = !some && below[i] == 256;
 #pragma unroll 1
       for (int p = p0; p < all; p += per * 32) {
-        const uint4 v = lds128(place(m, p));
+        uint4 v = lds128(place(m, p));
         uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t lo = word(v, j) & 0x7FFF, hi = (word(v, j) >> 16) & 0x7FFF;
-          left |= (lo < low && lo != 0) || (hi < low && hi != 0);
-          const float f0 = lo >= low && lo < lim ? bf16_lo(word(v, j)) * up : 0.f;
-          const float f1 = hi >= low && hi < lim ? bf16_hi(word(v, j)) * up : 0.f;
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(f1), "f"(f0));
+        if (!whole_row) {
+          v.x = in_window(v.x, low, lim);
+          v.y = in_window(v.y, low, lim);
+          v.z = in_window(v.z, low, lim);
+          v.w = in_window(v.w, low, lim);
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+              : "=r"(o[j]) : "f"(bf16_hi(word(v, j)) * up), "f"(bf16_lo(word(v, j)) * up));
         sts128(place(m, p), o[0], o[1], o[2], o[3]);
       }
       below[i] = max(high - 28, 0);
