@@ -613,6 +613,15 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
           } else {
             tmem_load_x32(base + j + 32 * h, v);
             tmem_wait_load();
+            // The columns that the next tile waits for have been read.
+            if (i == (BN == 256 ? 0 : BN - width) && h == width / 32 - 1) {
+              tc_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) {
+                if constexpr (CTAS == 2) mbar_arrive_cluster(cluster_addr(acc_empty + 8 * s, 0));
+                else mbar_arrive(acc_empty + 8 * s);
+              }
+            }
           }
           const uint32_t line = patch + lane * 128;
           if (a.out_f32) {
@@ -633,12 +642,7 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
           }
         }
         fence_proxy_async_smem();
-        tc_fence_before_sync();
         __syncwarp();
-        if (!empty_tile && lane == 0 && i == (BN == 256 ? 0 : BN - width)) {
-          if constexpr (CTAS == 2) mbar_arrive_cluster(cluster_addr(acc_empty + 8 * s, 0));
-          else mbar_arrive(acc_empty + 8 * s);
-        }
         if (!bulk) {
           store_patch(a, patch, lane, out_row, rows, tile.n0 + j, tile.cols - tile.n0 - j,
                       tile.add);
