@@ -222,13 +222,27 @@ __device__ __forceinline__ void store_patch(const GroupedArgs& a, uint32_t patch
     }
     return;
   }
+  // Eight rows are read before any is written: a row's way through shared
+  // memory takes longer than its store.
+  constexpr int BATCH = 8;
   if (a.out_f32) {
-    const int unit = lane / 4, in = lane % 4 * 4;
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r) {
-      float v = __uint_as_float(lds32(patch + r * 128 + ((unit ^ (r & 7)) << 4) + in));
-      float* p = static_cast<float*>(a.out) + (row + r) * a.ldo + col + lane;
-      if (r < rows && lane < cols) *p = add ? v + *p : v;
+    float* p = static_cast<float*>(a.out) + row * a.ldo + col + lane;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += BATCH) {
+      float v[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i)
+        v[i] = __uint_as_float(
+            lds32(patch + (r0 + i) * 128 + (((lane / 4) ^ (i & 7)) << 4) + lane % 4 * 4));
+      if (add) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+          if (r0 + i < rows && lane < cols) v[i] += p[i * a.ldo];
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i)
+        if (r0 + i < rows && lane < cols) p[i * a.ldo] = v[i];
+      p += BATCH * a.ldo;
     }
     return;
   }
@@ -237,19 +251,25 @@ __device__ __forceinline__ void store_patch(const GroupedArgs& a, uint32_t patch
   uint16_t* p = static_cast<uint16_t*>(a.out) + row * a.ldo + col;
   const int limit = min(cols, 64), skew = static_cast<int>(a.ldo & 1);
   const int odd0 = static_cast<int>((reinterpret_cast<uintptr_t>(p) / 2) & 1);
-#pragma unroll 8
-  for (int r = 0; r < 32; ++r) {
-    const int odd = odd0 ^ (skew & r);
-    const uint32_t v = lds32(patch + r * 128 + (((lane / 4) ^ (r & 7)) << 4) + lane % 4 * 4);
-    const uint32_t next = __shfl_down_sync(~0u, v, 1);
-    const int c = 2 * lane + odd;
-    if (r < rows) {
-      if (c + 1 < limit) stg32(p + c, odd ? v >> 16 | next << 16 : v);
-      if (odd && lane == 0 && limit > 0) p[0] = static_cast<uint16_t>(v);
-      if (((limit - odd) & 1) && limit > odd && lane == (limit - 1) / 2)
-        p[limit - 1] = static_cast<uint16_t>(limit & 1 ? v : v >> 16);
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += BATCH) {
+    uint32_t pair[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      pair[i] = lds32(patch + (r0 + i) * 128 + (((lane / 4) ^ (i & 7)) << 4) + lane % 4 * 4);
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int odd = odd0 ^ (skew & i);
+      const uint32_t v = pair[i], next = __shfl_down_sync(~0u, v, 1);
+      const int c = 2 * lane + odd;
+      if (r0 + i < rows) {
+        if (c + 1 < limit) stg32(p + c, odd ? v >> 16 | next << 16 : v);
+        if (odd && lane == 0 && limit > 0) p[0] = static_cast<uint16_t>(v);
+        if (((limit - odd) & 1) && limit > odd && lane == (limit - 1) / 2)
+          p[limit - 1] = static_cast<uint16_t>(limit & 1 ? v : v >> 16);
+      }
+      p += a.ldo;
     }
-    p += a.ldo;
   }
 }
 
