@@ -626,21 +626,43 @@ struct Plan {
   int tiles, cluster, cap;
 };
 
-// Tiles of 8 * 16 columns wherever they make items enough for three CTAs on two
-// SMs: a part of K less is a copy less, and sums less to add.  Where they do
-// not, K is split: inside the CTA for one or two rows (28672 x 8192 weights, one
-// row: 34 us in halves, 38 whole, 36 over clusters of two), over clusters for
-// more, whose staged rows the CTAs of a cluster then share out (4099 x 11008,
-// thirteen rows: 22 us over clusters of 8, 84 in one CTA, 34 in halves).
+// One or two rows: of the cuts into 1, 2, 4 or 8 tiles an item, 8, 4, 2 or 1
+// parts of K, the one with the least estimated time.  Few parts mean few copies
+// and sums an item, many items an even load: 28672 x 8192 weights, one row, 36,
+// 33.7, 32.4 and 35.8 us with 8, 4, 2 and 1 tiles; 38912 x 8192, an item of 8 a
+// CTA, 38, 39, 41 and 45.  K over clusters only where even one tile an item leaves
+// SMs free.
+//
+// More rows: 8 tiles, and K over clusters of the size with the least estimated
+// time, so that the staged rows are shared out too (4099 x 11008 weights, thirteen
+// rows: 17.4 us over clusters of 8, 84 in one CTA, 34 in halves; 14336 x 4096, four
+// rows: 18.1, 14.5 and 19.2 us over clusters of 1, 2 and 4).
 Plan choose(const GemvArgs& a, int rows, int toks, int x_bytes, int64_t slots, int num_sms) {
   const int64_t steps = (a.k + STEP_K - 1) / STEP_K;
   auto items = [&](int tiles) { return (a.n + tiles * 16 - 1) / (tiles * 16) * slots; };
   Plan plan{WARPS, 1, a.experts || a.rows > toks ? toks : a.rows};
-  const int64_t want = num_sms * 3 / 2;
-  while (rows <= 2 && plan.tiles > 1 && items(plan.tiles) < want) plan.tiles /= 2;
-  while (plan.cluster < 8 && items(plan.tiles) * plan.cluster < want &&
-         steps >= 2 * plan.cluster * (WARPS / plan.tiles))
-    plan.cluster *= 2;
+  // Quarters of a round of two CTAs an SM; a last one of at most a CTA an SM takes
+  // three.
+  auto rounds = [&](int64_t n) {
+    const int64_t rest = n % (2 * num_sms);
+    return n / (2 * num_sms) * 4 + (rest > num_sms ? 4 : rest > 0 ? 3 : 0);
+  };
+  if (rows <= 2) {
+    // In eighths of a step of all warps, a step more an item.
+    auto cost = [&](int tiles) { return rounds(items(tiles)) * (steps * tiles + 8); };
+    for (int tiles = WARPS / 2; tiles > 0; tiles /= 2)
+      if (cost(tiles) < cost(plan.tiles)) plan.tiles = tiles;
+    while (plan.tiles == 1 && plan.cluster < 8 && items(1) * plan.cluster < num_sms * 3 / 2 &&
+           steps >= 2 * WARPS * plan.cluster)
+      plan.cluster *= 2;
+  } else {
+    // Staging and the sums over a cluster are worth four steps.
+    auto cost = [&](int cluster) {
+      return rounds(items(WARPS) * cluster) * (8 * steps / cluster + 32);
+    };
+    for (int cluster = 2; cluster <= 8 && cluster <= steps; cluster *= 2)
+      if (cost(cluster) <= cost(plan.cluster)) plan.cluster = cluster;
+  }
   while (plan.tiles > 1 && items(plan.tiles) * plan.cluster < num_sms / 2) plan.tiles /= 2;
   // Rows whose range of K is staged whole, if that takes all that are expected.
   const int64_t range = (steps + plan.cluster - 1) / plan.cluster;
