@@ -12,6 +12,8 @@
 // few rows an expert by reading the weights (36 rows over 41 experts, 5866 x
 // 1344: 34 us, 5.8 TB/s), weight gradients of short groups by writing them (64
 // experts x 1408 x 2048 fp32: 135 us, 5.7 TB/s).
+#include <type_traits>
+
 #include "mxq_products.h"
 
 #include "mxq_tc_ptx.cuh"
@@ -194,9 +196,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // the output at `col`; `cols` columns exist.  Whole patches of 16-byte aligned
 // rows leave as full 128-byte lines (four rows an instruction), others by
 // elements, a row at a time.
+template <bool F32>
 __device__ __forceinline__ void store_patch(const GroupedArgs& a, uint32_t patch, int lane,
                                             int64_t row, int rows, int col, int cols, bool add) {
-  const int width = a.out_f32 ? 32 : 64;
+  constexpr int width = F32 ? 32 : 64;
   if (a.out_vec && cols >= width) {
     const int u = lane % 8;
 #pragma unroll
@@ -204,7 +207,7 @@ __device__ __forceinline__ void store_patch(const GroupedArgs& a, uint32_t patch
       const int r = 4 * i + lane / 8;
       uint4 v = lds128(patch + r * 128 + ((u ^ (r & 7)) << 4));
       if (r < rows) {
-        if (a.out_f32) {
+        if constexpr (F32) {
           float* p = static_cast<float*>(a.out) + (row + r) * a.ldo + col + 4 * u;
           if (add) {
             const float4 o = *reinterpret_cast<const float4*>(p);
@@ -225,7 +228,7 @@ __device__ __forceinline__ void store_patch(const GroupedArgs& a, uint32_t patch
   // Eight rows are read before any is written: a row's way through shared
   // memory takes longer than its store.
   constexpr int BATCH = 8;
-  if (a.out_f32) {
+  if constexpr (F32) {
     float* p = static_cast<float*>(a.out) + row * a.ldo + col + lane;
 #pragma unroll 1
     for (int r0 = 0; r0 < rows; r0 += BATCH) {
@@ -618,61 +621,75 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
         continue;
       }
       const uint32_t base = tmem + S::acc_col(s) + (static_cast<uint32_t>(warp) << 21);
-      for (int i = 0; i < BN; i += width) {
-        // Accumulator 0 shares its last 32 columns with the next tile's
-        // first 32: they are read first.
-        const int j = BN == 256 && s == 0 ? BN - width - i : i;
-        const uint32_t patch = patches + (warp * S::PATCHES + turn++ % (S::PATCHES ? S::PATCHES : 1)) * 4096;
-        if (lane == 0) bulk_wait_read<S::PATCHES ? S::PATCHES - 1 : 0>();
-        __syncwarp();
-        for (int h = 0; h < width / 32; ++h) {
-          uint32_t v[32];
-          if (empty_tile) {
+      // The loop for each way out and type, so that the one of whole patches, which
+      // bounds short contractions, stays small.
+      auto drain = [&](auto whole, auto wide) {
+        constexpr bool BULK = decltype(whole)::value, F32 = decltype(wide)::value;
+        constexpr int WIDTH = F32 ? 32 : 64;             // columns of a patch
+#pragma unroll 1
+        for (int i = 0; i < BN; i += WIDTH) {
+          // Accumulator 0 shares its last 32 columns with the next tile's
+          // first 32: they are read first.
+          const int j = BN == 256 && s == 0 ? BN - WIDTH - i : i;
+          const uint32_t patch =
+              patches + (warp * S::PATCHES + turn++ % (S::PATCHES ? S::PATCHES : 1)) * 4096;
+          if (lane == 0) bulk_wait_read<S::PATCHES ? S::PATCHES - 1 : 0>();
+          __syncwarp();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = 0;
-          } else {
-            tmem_load_x32(base + j + 32 * h, v);
-            tmem_wait_load();
-            // The columns that the next tile waits for have been read.
-            if (i == (BN == 256 ? 0 : BN - width) && h == width / 32 - 1) {
-              tc_fence_before_sync();
-              __syncwarp();
-              if (lane == 0) {
-                if constexpr (CTAS == 2) mbar_arrive_cluster(cluster_addr(acc_empty + 8 * s, 0));
-                else mbar_arrive(acc_empty + 8 * s);
+          for (int h = 0; h < WIDTH / 32; ++h) {
+            uint32_t v[32];
+            if (!BULK && empty_tile) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[c] = 0;
+            } else {
+              tmem_load_x32(base + j + 32 * h, v);
+              tmem_wait_load();
+              // The columns that the next tile waits for have been read.
+              if (i == (BN == 256 ? 0 : BN - WIDTH) && h == WIDTH / 32 - 1) {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                  if constexpr (CTAS == 2) mbar_arrive_cluster(cluster_addr(acc_empty + 8 * s, 0));
+                  else mbar_arrive(acc_empty + 8 * s);
+                }
+              }
+            }
+            const uint32_t line = patch + lane * 128;
+            if constexpr (F32) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                sts128(line + ((u ^ (lane & 7)) << 4), v[4 * u], v[4 * u + 1], v[4 * u + 2],
+                       v[4 * u + 3]);
+            } else {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                uint32_t w[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  w[c] = pack_bf16(__uint_as_float(v[8 * u + 2 * c]),
+                                   __uint_as_float(v[8 * u + 2 * c + 1]));
+                sts128(line + (((4 * h + u) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
               }
             }
           }
-          const uint32_t line = patch + lane * 128;
-          if (a.out_f32) {
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              sts128(line + ((u ^ (lane & 7)) << 4), v[4 * u], v[4 * u + 1], v[4 * u + 2],
-                     v[4 * u + 3]);
-          } else {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              uint32_t w[4];
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                w[c] = pack_bf16(__uint_as_float(v[8 * u + 2 * c]),
-                                 __uint_as_float(v[8 * u + 2 * c + 1]));
-              sts128(line + (((4 * h + u) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
-            }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if constexpr (!BULK) {
+            store_patch<F32>(a, patch, lane, out_row, rows, tile.n0 + j, tile.cols - tile.n0 - j,
+                             tile.add);
+          } else if (lane == 0 && tile.n0 + j < tile.cols) {
+            const int y = KIND == WGRAD ? first : static_cast<int>(out_row);
+            const int z = KIND == WGRAD ? tile.g : 0;
+            if (F32 && tile.add) tma_add_3d(&maps.out, patch, tile.n0 + j, y, z);
+            else tma_store_3d(&maps.out, patch, tile.n0 + j, y, z);
           }
+          if (lane == 0) bulk_commit();       // one group a patch, empty ones too
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (!bulk) {
-          store_patch(a, patch, lane, out_row, rows, tile.n0 + j, tile.cols - tile.n0 - j,
-                      tile.add);
-        } else if (lane == 0 && tile.n0 + j < tile.cols) {
-          const int y = KIND == WGRAD ? first : static_cast<int>(out_row), z = KIND == WGRAD ? tile.g : 0;
-          if (tile.add) tma_add_3d(&maps.out, patch, tile.n0 + j, y, z);
-          else tma_store_3d(&maps.out, patch, tile.n0 + j, y, z);
-        }
-        if (lane == 0) bulk_commit();       // one group a patch, empty ones too
-      }
+      };
+      if (bulk && a.out_f32) drain(std::true_type{}, std::true_type{});
+      else if (bulk) drain(std::true_type{}, std::false_type{});
+      else if (a.out_f32) drain(std::false_type{}, std::true_type{});
+      else drain(std::false_type{}, std::false_type{});
     }
     if (lane == 0) bulk_wait_all();
   }
