@@ -588,16 +588,22 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
           if (!empty_tile && lane == 0 && j == BN - 32) mbar_arrive(acc_empty + 8 * s);
           const int count = lane < rows ? tile.cols - tile.n0 - j : 0;
           const int64_t at = (static_cast<int64_t>(tile.by) + tile.n0 + j) * a.ldo + first + lane;
+          if (a.out_f32) {
+            float* p = static_cast<float*>(a.out) + at;
+            if (tile.add) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (c >= count) continue;
-            if (a.out_f32) {
-              float* p = static_cast<float*>(a.out) + at + c * a.ldo;
-              *p = tile.add ? __uint_as_float(v[c]) + *p : __uint_as_float(v[c]);
-            } else {
-              static_cast<uint16_t*>(a.out)[at + c * a.ldo] =
-                  static_cast<uint16_t>(pack_bf16(__uint_as_float(v[c]), 0.f));
+              for (int c = 0; c < 32; ++c)
+                if (c < count) v[c] = __float_as_uint(__uint_as_float(v[c]) + p[c * a.ldo]);
             }
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c < count) p[c * a.ldo] = __uint_as_float(v[c]);
+          } else {
+            uint16_t* p = static_cast<uint16_t*>(a.out) + at;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c < count)
+                p[c * a.ldo] = static_cast<uint16_t>(pack_bf16(__uint_as_float(v[c]), 0.f));
           }
         }
         continue;
