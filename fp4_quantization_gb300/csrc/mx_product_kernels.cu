@@ -39,6 +39,13 @@ constexpr int FEW_ROWS = 32;
 // rounding them, which is 6.4e-7 of the result after this many values, twice
 // that after twice as many.
 constexpr int SEGMENT = 8192;
+// Ranges of the contraction that the CTAs of a cluster take at most, and the
+// stages of one at least (16 rows x 4096 x 14336: 32.4 us whole, 20.9 in halves,
+// 15.7 in quarters, 15.8 in eighths; 8 x 2048 x 2048, 16 stages, 8.1, 7.2, 6.2).
+// Adding them up takes as long as some four stages: 8 are not divided (128 x 512 x
+// 1024 6.9 us whole, 8.6 in halves).
+constexpr int SPLIT_MAX = 4;
+constexpr int SPLIT_STEPS = 4;
 
 // What the two operands and the output tile are.
 //  FORWARD: A the rows of x of a group, B its expert's weight.
@@ -96,8 +103,9 @@ struct Tile {
 // Walks the tiles of this CTA (or pair) in order.  Inside a group the row
 // tiles of a band of 2048 rows run fastest, so a wave's tiles share their rows
 // and each column tile's codes come from memory once a band; with few rows of
-// x, all of them beside each weight tile.
-template <int CTAS, int BN, int KIND>
+// x, all of them beside each weight tile.  With SPLIT the CTAs of a cluster take
+// a range of the contraction each, of one tile.
+template <int CTAS, int BN, int KIND, bool SPLIT = false>
 struct Walk {
   const int* off;
   const int* start;     // first tile of each group, and the total
@@ -119,6 +127,12 @@ struct Walk {
     tile.add = done > 0;
     tile.first = tile.add ? done : from;
     tile.end = a.out_f32 ? min(to, (tile.first / STEP_K + SEGMENT / STEP_K) * STEP_K) : to;
+    if constexpr (SPLIT) {
+      const int each = ((to + STEP_K - 1) / STEP_K + a.split - 1) / a.split * STEP_K;
+      tile.first = min(static_cast<int>(cluster_rank()) * each, to);
+      tile.end = to - tile.first > each ? tile.first + each : to;
+      tile.add = false;
+    }
     const int tiles_n = (tile.cols + BN - 1) / BN;
     int i = t - start[g];
     if constexpr (KIND == FEW) {
@@ -134,7 +148,7 @@ struct Walk {
       tile.n0 = i / height * BN;
     }
     done = tile.end;
-    if (done == to) {
+    if (SPLIT || done == to) {
       done = 0;
       t += gridDim.x / CTAS;
     }
@@ -276,7 +290,11 @@ __device__ __forceinline__ void store_patch(const GroupedArgs& a, uint32_t patch
   }
 }
 
-template <int CTAS, int BN, int KIND>
+// Floats of a row of a part of a FORWARD tile's sums in shared memory: lanes that
+// write 16 bytes of neighbouring rows meet no bank twice.
+constexpr int PART_LD = 128 + 4;
+
+template <int CTAS, int BN, int KIND, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
 mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a) {
   using S = Shape<CTAS, BN>;
@@ -358,7 +376,8 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
-  Walk<CTAS, BN, KIND> walk{off, start, a.groups, static_cast<int>(blockIdx.x) / CTAS, 0, 0};
+  const int tile0 = static_cast<int>(blockIdx.x) / (SPLIT ? a.split : CTAS);
+  Walk<CTAS, BN, KIND, SPLIT> walk{off, start, a.groups, tile0, 0, 0};
   Tile tile;
   bool ok = true;
 
@@ -571,7 +590,31 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
         tc_fence_after_sync();
         ++acc;
       }
-      if constexpr (KIND == FEW) {
+      if constexpr (SPLIT) {
+        // The range's sums, where the stages were: columns of 128 rows (FEW), rows of
+        // PART_LD columns.  The tile's instructions, its last, are complete.
+        const uint32_t from = tmem + S::acc_col(s) + (static_cast<uint32_t>(warp) << 21);
+        const int r = warp * 32 + lane;
+#pragma unroll 1
+        for (int j = 0; j < BN; j += 32) {
+          uint32_t v[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = 0;
+          if (!empty_tile) {
+            tmem_load_x32(from + j, v);
+            tmem_wait_load();
+          }
+          if constexpr (KIND == FEW) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) sts32(stages + ((j + c) * ROWS + r) * 4, v[c]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; c += 4)
+              sts128(stages + (r * PART_LD + j + c) * 4, v[c], v[c + 1], v[c + 2], v[c + 3]);
+          }
+        }
+        continue;
+      } else if constexpr (KIND == FEW) {
         // The lanes hold 32 neighbouring columns of a row of the output, row by row.
         const uint32_t from = tmem + S::acc_col(s) + (static_cast<uint32_t>(warp) << 21);
 #pragma unroll 1
@@ -703,37 +746,128 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
   if (!ok && a.dev_err) atomicOr(a.dev_err, MXQ_DEVERR_TIMEOUT);
   tc_fence_before_sync();
   __syncthreads();
-  // A pair's CTAs leave together: each arrives on the other's barriers.
-  if constexpr (CTAS == 2) cluster_sync();
+  if constexpr (SPLIT) {
+    // Every CTA adds its share of the tile, the ranges in order.
+    cluster_sync();
+    Walk<CTAS, BN, KIND, SPLIT> again{off, start, a.groups, tile0, 0, 0};
+    if (again.next(a, tile)) {
+      const int part = static_cast<int>(cluster_rank());
+      const int rows = min(ROWS, tile.rows - tile.m0), cols = min(BN, tile.cols - tile.n0);
+      if constexpr (KIND == FEW) {
+        const int r = tid % ROWS;
+        constexpr int AT_ONCE = THREADS / ROWS;
+        if (tid < AT_ONCE * ROWS && r < rows) {
+#pragma unroll 2
+          for (int c = tid / ROWS * a.split + part; c < cols; c += AT_ONCE * a.split) {
+            const uint32_t at = stages + (c * ROWS + r) * 4;
+            float v[SPLIT_MAX], sum = 0;
+#pragma unroll
+            for (int p = 0; p < SPLIT_MAX; ++p) v[p] = p < a.split ? ld_cluster_f32(at, p) : 0.f;
+#pragma unroll
+            for (int p = 0; p < SPLIT_MAX; ++p) sum += v[p];
+            const int64_t to = (static_cast<int64_t>(tile.by) + tile.n0 + c) * a.ldo + tile.m0 + r;
+            if (a.out_f32) static_cast<float*>(a.out)[to] = sum;
+            else
+              static_cast<uint16_t*>(a.out)[to] = static_cast<uint16_t>(pack_bf16(sum, 0.f));
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int r = warp * a.split + part; r < rows; r += THREADS / 32 * a.split) {
+          const uint32_t at = stages + (r * PART_LD + 4 * lane) * 4;
+          float4 v[SPLIT_MAX];
+#pragma unroll
+          for (int p = 0; p < SPLIT_MAX; ++p)
+            v[p] = p < a.split ? ld_cluster_f32x4(at, p) : make_float4(0.f, 0.f, 0.f, 0.f);
+          float sum[4] = {};
+#pragma unroll
+          for (int p = 0; p < SPLIT_MAX; ++p) {
+            sum[0] += v[p].x;
+            sum[1] += v[p].y;
+            sum[2] += v[p].z;
+            sum[3] += v[p].w;
+          }
+          const int left = cols - 4 * lane;
+          const int64_t to = (static_cast<int64_t>(tile.ay) + tile.m0 + r) * a.ldo + tile.n0 + 4 * lane;
+          if (a.out_f32) {
+            float* p = static_cast<float*>(a.out) + to;
+            if (a.out_vec && left >= 4) {
+              *reinterpret_cast<float4*>(p) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (c < left) p[c] = sum[c];
+            }
+          } else {
+            uint16_t* p = static_cast<uint16_t*>(a.out) + to;
+            const uint32_t lo = pack_bf16(sum[0], sum[1]), hi = pack_bf16(sum[2], sum[3]);
+            if (a.out_vec && left >= 4) {
+              *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (c < left) p[c] = static_cast<uint16_t>((c < 2 ? lo : hi) >> (c % 2 * 16));
+            }
+          }
+        }
+      }
+    }
+  }
+  // A cluster's CTAs leave together: each arrives on the other's barriers, or reads
+  // its sums.
+  if constexpr (CTAS == 2 || SPLIT) cluster_sync();
   tc_fence_after_sync();
   if (warp == 9) tmem_dealloc<CTAS>(tmem, TMEM_COLS);
 }
 
-template <int CTAS, int BN, int KIND>
+// CTAs that share a tile's contraction, where there are fewer tiles than SMs (of
+// which clusters of four reach 144).
+int ranges(const GroupedArgs& a, int64_t tiles, int num_sms) {
+  const int steps = (a.depth + STEP_K - 1) / STEP_K;
+  int split = 1;
+  while (split < SPLIT_MAX && steps >= 4 * SPLIT_STEPS && steps >= 2 * split * SPLIT_STEPS &&
+         tiles * 2 * split * 64 <= num_sms * (64 - 2 * split))
+    split *= 2;
+  // Sums of more than SEGMENT values are taken apart by the other kernel.
+  return a.out_f32 && (steps + split - 1) / split * STEP_K > SEGMENT ? 1 : split;
+}
+
+template <int CTAS, int BN, int KIND, bool SPLIT = false>
 cudaError_t launch(const GroupedMaps& maps, const GroupedArgs& a, int num_sms,
                    cudaStream_t stream) {
-  auto kernel = mx_grouped_kernel<CTAS, BN, KIND>;
+  auto kernel = mx_grouped_kernel<CTAS, BN, KIND, SPLIT>;
   constexpr int smem = Shape<CTAS, BN>::SMEM;
   static_assert(smem <= 227 * 1024, "shared memory of one SM");
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), smem, &allowed);
   if (e != cudaSuccess) return e;
-  // At most this many tiles, whatever the offsets are.
+  // At most this many tiles, whatever the offsets are: every group has a row more
+  // than whole tiles.
   constexpr int TILE_M = ROWS * CTAS;
-  auto split = [&](int tile) { return a.limit / tile + (a.groups < a.limit ? a.groups : a.limit); };
+  const int64_t used = a.groups < a.limit ? a.groups : a.limit;
+  auto split = [&](int tile) { return (a.limit - used) / tile + used; };
   auto whole = [](int64_t n, int tile) { return (n + tile - 1) / tile; };
   const int64_t tiles = KIND == FORWARD ? split(TILE_M) * whole(a.b_rows, BN)
                         : KIND == FEW   ? split(BN) * whole(a.a_rows, TILE_M)
                                         : a.groups * whole(a.a_rows, TILE_M) * whole(a.b_rows, BN);
-  const int64_t most = num_sms / CTAS;
+  if constexpr (CTAS == 1 && KIND != WGRAD && BN <= 128 && !SPLIT) {
+    const int split = ranges(a, tiles, num_sms);
+    if (split > 1) {
+      GroupedArgs b = a;
+      b.split = split;
+      return launch<CTAS, BN, KIND, true>(maps, b, num_sms, stream);
+    }
+  }
+  const int cluster = SPLIT ? a.split : CTAS;
+  const int64_t most = num_sms / cluster;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles < most ? tiles : most) * CTAS);
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles < most ? tiles : most) * cluster);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = CTAS;
+  attr.val.clusterDim.x = cluster;
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;

@@ -29,6 +29,7 @@ struct GroupedArgs {
   int a_rows;               // wgrad, few: N
   int b_rows;               // forward: N; wgrad: K
   int depth;                // forward: K
+  int split;                // CTAs of a cluster that share a tile's contraction (set by the launch)
   const uint8_t* a_s;       // E8M0 scales, s_ld bytes a row
   const uint8_t* b_s;
   int64_t s_ld;

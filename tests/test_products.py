@@ -136,6 +136,50 @@ def test_grouped_gemm(name, sizes, N, K, before, after, dtype, exact):
     check(out, want, bound, exact, name)
 
 
+# Few tiles of a long contraction: CTAs of a cluster share it.
+GEMM_SPLIT = [
+    ("one_row", [1], 200, 4096, 0, 0),
+    ("few_rows", [31], 1000, 8192 - 32, 1, 2),
+    ("few_experts", [3, 0, 9, 1], 513, 2048, 0, 0),
+    ("last_range_empty", [5], 128, 128 * 65, 0, 0),
+    ("dense", [60], 513, 4096, 3, 4),
+    ("dense_odd", [77, 0, 250], 267, 2080, 0, 0),
+    ("dense_aligned", [128, 256], 256, 16384, 0, 0),
+    ("all_empty", [0, 0], 64, 4096, 50, 50),
+]
+
+
+@gpu
+@pytest.mark.parametrize("exact", [True, False], ids=["exact", "random"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("name,sizes,N,K,before,after", GEMM_SPLIT, ids=[c[0] for c in GEMM_SPLIT])
+def test_grouped_gemm_shared_contraction(name, sizes, N, K, before, after, dtype, exact):
+    test_grouped_gemm(name, sizes, N, K, before, after, dtype, exact)
+
+
+@gpu
+def test_grouped_gemm_shared_contraction_in_place():
+    """A view at an odd element, the same bits every time, and nothing written
+    where the offsets are wrong."""
+    gen = generator(6)
+    for M, N, K in ((20, 300, 4096), (90, 300, 4096)):
+        x_q, x_s = mx_operand(gen, False, M, K)
+        w_q, w_s = mx_operand(gen, False, 1, N, K)
+        for dtype in (torch.bfloat16, torch.float32):
+            first = mxq.mx_grouped_gemm(x_q, x_s, w_q, w_s, offsets_of([M]), out_dtype=dtype)
+            whole = torch.full((M, N + 7), 9.0, dtype=dtype, device="cuda")
+            for at in (0, 3, 4):
+                whole.fill_(9)
+                mxq.mx_grouped_gemm(x_q, x_s, w_q, w_s, offsets_of([M]), out=whole[:, at:at + N])
+                assert (whole[:, at:at + N] == first).all()
+                assert (whole[:, :at] == 9).all() and (whole[:, at + N:] == 9).all()
+            err = dev_err()
+            whole.fill_(9)
+            mxq.mx_grouped_gemm(x_q, x_s, w_q, w_s, offsets_of([M + 1]), out=whole[:, :N],
+                                dev_err=err)
+            assert err.item() == mxq.DEVERR_OFFSETS and (whole == 9).all()
+
+
 @gpu
 def test_grouped_gemm_strided_output_and_stream():
     """An output inside a wider matrix, at an odd element, on another stream;
