@@ -256,8 +256,11 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
   uint32_t scale[DEPTH][2][2] = {};                   // four scales a row, or two and two apart
   uint32_t phase = 0, used = 0, pending = 0;          // a bit a place
   bool ok = true;                                     // no wait of the warp ran out
+  const int whole_to = words ? a.k - STEP_K : -1;     // a step from here has all its scales
+  int load_end = 0;
   auto load_start = [&] {
     load_k = start_of(load_k0);
+    load_end = load_item < item_end ? min(load_k0 + room, k_end) : 0;
     if (load_item >= item_end) return;
     const Item item = item_at(load_item);
     const int n = item.n0 + tile * 16;
@@ -268,8 +271,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
              4 * t;
   };
   auto load_next = [&](int i, uint32_t (&v)[2][2]) {
-    const int k1 = min(load_k0 + room, k_end);
-    if (ok && load_item < item_end && load_k < k1) {
+    if (ok && load_k < load_end) {
       if (tile == 0) {
         // The place has been read by all the part's warps.
         if (used >> i & 1) {
@@ -282,7 +284,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
       }
       used |= 1u << i;
       pending |= 1u << i;
-      if (words && load_k + STEP_K <= a.k) {
+      if (load_k <= whole_to) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           v[h][0] = __ldg(reinterpret_cast<const uint32_t*>(s[h] + load_k / 16));
@@ -300,7 +302,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
       }
     }
     load_k += turn;
-    if (i == DEPTH - 1 && load_k >= k1) {
+    if (i == DEPTH - 1 && load_k >= load_end) {
       load_k0 += room;
       if (load_k0 >= k_end) {
         load_k0 = k_first;
