@@ -128,9 +128,12 @@ struct Walk {
     tile.first = tile.add ? done : from;
     tile.end = a.out_f32 ? min(to, (tile.first / STEP_K + SEGMENT / STEP_K) * STEP_K) : to;
     if constexpr (SPLIT) {
-      const int each = ((to + STEP_K - 1) / STEP_K + a.split - 1) / a.split * STEP_K;
-      tile.first = min(static_cast<int>(cluster_rank()) * each, to);
-      tile.end = to - tile.first > each ? tile.first + each : to;
+      // Whole stages, so that no two CTAs copy the same one.
+      const int step0 = from / STEP_K, steps = (to + STEP_K - 1) / STEP_K - step0;
+      const int each = (steps + a.split - 1) / a.split;
+      const int at = step0 + min(static_cast<int>(cluster_rank()) * each, steps);
+      tile.first = min(max(at * STEP_K, from), to);
+      tile.end = min(min(at + each, step0 + steps) * STEP_K, to);
       tile.add = false;
     }
     const int tiles_n = (tile.cols + BN - 1) / BN;
@@ -789,7 +792,9 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
             sum[3] += v[p].w;
           }
           const int left = cols - 4 * lane;
-          const int64_t to = (static_cast<int64_t>(tile.ay) + tile.m0 + r) * a.ldo + tile.n0 + 4 * lane;
+          const int64_t row = KIND == WGRAD ? static_cast<int64_t>(tile.g) * a.a_rows
+                                            : static_cast<int64_t>(tile.ay);
+          const int64_t to = (row + tile.m0 + r) * a.ldo + tile.n0 + 4 * lane;
           if (a.out_f32) {
             float* p = static_cast<float*>(a.out) + to;
             if (a.out_vec && left >= 4) {
@@ -821,16 +826,17 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
   if (warp == 9) tmem_dealloc<CTAS>(tmem, TMEM_COLS);
 }
 
-// CTAs that share a tile's contraction, where there are fewer tiles than SMs (of
-// which clusters of four reach 144).
-int ranges(const GroupedArgs& a, int64_t tiles, int num_sms) {
-  const int steps = (a.depth + STEP_K - 1) / STEP_K;
+// CTAs that share a tile's contraction, of `depth` values on average and `most` at
+// most, where there are fewer tiles than SMs (of which clusters of four reach 144).
+int ranges(const GroupedArgs& a, int depth, int most, int64_t tiles, int num_sms) {
+  const int steps = (depth + STEP_K - 1) / STEP_K;
   int split = 1;
   while (split < SPLIT_MAX && steps >= 4 * SPLIT_STEPS && steps >= 2 * split * SPLIT_STEPS &&
          tiles * 2 * split * 64 <= num_sms * (64 - 2 * split))
     split *= 2;
   // Sums of more than SEGMENT values are taken apart by the other kernel.
-  return a.out_f32 && (steps + split - 1) / split * STEP_K > SEGMENT ? 1 : split;
+  const int each = ((most + STEP_K - 1) / STEP_K + split) / split * STEP_K;
+  return a.out_f32 && each > SEGMENT + STEP_K ? 1 : split;
 }
 
 template <int CTAS, int BN, int KIND, bool SPLIT = false>
@@ -851,8 +857,9 @@ cudaError_t launch(const GroupedMaps& maps, const GroupedArgs& a, int num_sms,
   const int64_t tiles = KIND == FORWARD ? split(TILE_M) * whole(a.b_rows, BN)
                         : KIND == FEW   ? split(BN) * whole(a.a_rows, TILE_M)
                                         : a.groups * whole(a.a_rows, TILE_M) * whole(a.b_rows, BN);
-  if constexpr (CTAS == 1 && KIND != WGRAD && BN <= 128 && !SPLIT) {
-    const int split = ranges(a, tiles, num_sms);
+  if constexpr (CTAS == 1 && BN <= 128 && !SPLIT) {
+    const int split = KIND == WGRAD ? ranges(a, a.limit / a.groups, a.limit, tiles, num_sms)
+                                    : ranges(a, a.depth, a.depth, tiles, num_sms);
     if (split > 1) {
       GroupedArgs b = a;
       b.split = split;

@@ -338,6 +338,25 @@ def test_grouped_wgrad(name, sizes, N, K, before, after, dtype, exact):
               rows * 2.0 ** -23 * (g[:, a:b].abs() @ x[:, a:b].abs().t()), exact, f"{name} {e}")
 
 
+# Few tiles of long groups: CTAs of a cluster share their rows.
+WGRAD_SPLIT = [
+    ("one_tile", [4096], 100, 128, 0, 0),
+    ("odd_start", [2048 + 32, 3200, 64], 129, 65, 32, 96),
+    ("one_long", [0, 8000, 32, 0], 64, 200, 64, 0),
+    ("halves", [5120], 640, 520, 0, 0),
+    ("last_range_empty", [128 * 65], 72, 80, 0, 0),
+    ("all_empty", [0, 0], 40, 40, 4096, 4096),
+]
+
+
+@gpu
+@pytest.mark.parametrize("exact", [True, False], ids=["exact", "random"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("name,sizes,N,K,before,after", WGRAD_SPLIT, ids=[c[0] for c in WGRAD_SPLIT])
+def test_grouped_wgrad_shared_contraction(name, sizes, N, K, before, after, dtype, exact):
+    test_grouped_wgrad(name, sizes, N, K, before, after, dtype, exact)
+
+
 @gpu
 def test_grouped_wgrad_keeps_nan_where_it_is():
     """NaN codes and scales in the 32 rows after a group's end, which share a
