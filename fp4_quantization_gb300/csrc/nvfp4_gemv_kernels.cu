@@ -717,8 +717,11 @@ cudaError_t launch_nvfp4_gemv(const GemvArgs& a, int num_sms, cudaStream_t strea
   // At most this many experts have rows, and then this many rows each.
   const int64_t slots = !a.experts ? 1 : a.rows < a.num_experts ? a.rows : a.num_experts;
   const int rows = a.experts ? static_cast<int>((a.rows + slots - 1) / slots) : a.rows;
-  return rows > 8 ? launch<16>(a, rows < 16 ? rows : 16, slots, num_sms, stream)
-                  : launch<8>(a, rows, slots, num_sms, stream);
+  // With more than 4 rows an expert on average some have more than 8, and would read
+  // their weights twice (7 experts with 52 rows, 16455 x 960: 35 us sixteen rows at a
+  // time, 55 eight; 11 with 36, 4633 x 4608: 90 and 54).
+  return rows > (a.experts ? 4 : 8) ? launch<16>(a, rows < 16 ? rows : 16, slots, num_sms, stream)
+                                    : launch<8>(a, rows, slots, num_sms, stream);
 }
 
 }  // namespace mxq
