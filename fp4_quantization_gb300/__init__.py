@@ -35,6 +35,9 @@ OP_ROWCOL = 0
 OP_NVFP4 = 1
 OP_DACT = 2
 OP_ROWCOL_HOST = 3
+OP_GROUPED_GEMM = 4
+OP_GROUPED_WGRAD = 5
+OP_NVFP4_GEMV = 6
 DEVERR_TIMEOUT = 1
 DEVERR_OFFSETS = 2
 
@@ -436,6 +439,22 @@ def nvfp4_gemv(x, w_q, w_s, global_scale, *, experts=None, share=1, out=None,
         N, K, E, flags, out.data_ptr(), ldo, _err_ptr(dev_err), _raw_stream(stream, x))
     _check(st, "nvfp4_gemv")
     return out
+
+
+_PLAN_FIELDS = {OP_GROUPED_GEMM: ("ctas", "cols", "few", "split", "tiles", "grid"),
+                OP_GROUPED_WGRAD: ("ctas", "cols", "few", "split", "tiles", "grid"),
+                OP_NVFP4_GEMV: ("toks", "tiles", "cluster", "cap", "items", "grid")}
+
+
+def mxq_product_plan(op, M, N, K, E, flags=0, *, num_sms=None):
+    """How a product's call is cut on a GPU of num_sms SMs (the current device's
+    by default; with num_sms no device is needed), as a dict; see include/mxq.h.
+    OP_NVFP4_GEMV takes M = T * share, and E = 0 for a call without experts."""
+    if num_sms is None:
+        num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    plan = (ctypes.c_int32 * 6)()
+    _check(_lib.lib().mxq_product_plan(op, M, N, K, E, flags, num_sms, plan), "mxq_product_plan")
+    return dict(zip(_PLAN_FIELDS[op], plan))
 
 
 def mxq_selftest_bounded_wait(timeout_ns, dev_err, *, stream=None):

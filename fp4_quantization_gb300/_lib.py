@@ -41,6 +41,8 @@ SIGNATURES = {
                                         _vp, _vp, _vp]),
     "nvfp4_gemv": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64,
                                   _u32, _vp, _i64, _vp, _vp]),
+    "mxq_product_plan": (ctypes.c_int, [ctypes.c_int, _i64, _i64, _i64, _i64, _u32, ctypes.c_int,
+                                        ctypes.POINTER(ctypes.c_int32)]),
     "mxq_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_uint64, _vp, _vp]),
 }
 

@@ -850,19 +850,19 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
 
 // CTAs that share a tile's contraction, of `depth` values on average and `most` at
 // most, where there are fewer tiles than SMs (of which clusters of four reach 144).
-int ranges(const GroupedArgs& a, int depth, int most, int64_t tiles, int num_sms) {
-  const int steps = (depth + STEP_K - 1) / STEP_K;
+int ranges(int64_t depth, int64_t most, int64_t tiles, bool out_f32, int num_sms) {
+  const int64_t steps = (depth + STEP_K - 1) / STEP_K;
   int split = 1;
   while (split < SPLIT_MAX && steps >= 4 * SPLIT_STEPS && steps >= 2 * split * SPLIT_STEPS &&
          tiles * 2 * split * 64 <= num_sms * (64 - 2 * split))
     split *= 2;
   // Sums of more than SEGMENT values are taken apart by the other kernel.
-  const int each = ((most + STEP_K - 1) / STEP_K + split) / split * STEP_K;
-  return a.out_f32 && each > SEGMENT + STEP_K ? 1 : split;
+  const int64_t each = ((most + STEP_K - 1) / STEP_K + split) / split * STEP_K;
+  return out_f32 && each > SEGMENT + STEP_K ? 1 : split;
 }
 
 template <int CTAS, int BN, int KIND, bool SPLIT = false>
-cudaError_t launch(const GroupedMaps& maps, const GroupedArgs& a, int num_sms,
+cudaError_t launch(const GroupedMaps& maps, const GroupedArgs& a, const GroupedPlan& plan,
                    cudaStream_t stream) {
   auto kernel = mx_grouped_kernel<CTAS, BN, KIND, SPLIT>;
   constexpr int smem = Shape<CTAS, BN>::SMEM;
@@ -870,28 +870,9 @@ cudaError_t launch(const GroupedMaps& maps, const GroupedArgs& a, int num_sms,
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), smem, &allowed);
   if (e != cudaSuccess) return e;
-  // At most this many tiles, whatever the offsets are: every group has a row more
-  // than whole tiles.
-  constexpr int TILE_M = ROWS * CTAS;
-  const int64_t used = a.groups < a.limit ? a.groups : a.limit;
-  auto split = [&](int tile) { return (a.limit - used) / tile + used; };
-  auto whole = [](int64_t n, int tile) { return (n + tile - 1) / tile; };
-  const int64_t tiles = KIND == FORWARD ? split(TILE_M) * whole(a.b_rows, BN)
-                        : KIND == FEW   ? split(BN) * whole(a.a_rows, TILE_M)
-                                        : a.groups * whole(a.a_rows, TILE_M) * whole(a.b_rows, BN);
-  if constexpr (CTAS == 1 && BN <= 128 && !SPLIT) {
-    const int split = KIND == WGRAD ? ranges(a, a.limit / a.groups, a.limit, tiles, num_sms)
-                                    : ranges(a, a.depth, a.depth, tiles, num_sms);
-    if (split > 1) {
-      GroupedArgs b = a;
-      b.split = split;
-      return launch<CTAS, BN, KIND, true>(maps, b, num_sms, stream);
-    }
-  }
-  const int cluster = SPLIT ? a.split : CTAS;
-  const int64_t most = num_sms / cluster;
+  const int cluster = SPLIT ? plan.split : CTAS;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles < most ? tiles : most) * cluster);
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.grid));
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -906,14 +887,13 @@ cudaError_t launch(const GroupedMaps& maps, const GroupedArgs& a, int num_sms,
 }
 
 template <int KIND>
-cudaError_t launch_plan(GroupedPlan plan, const GroupedMaps& maps, const GroupedArgs& a,
-                        int num_sms, cudaStream_t stream) {
-  if (plan.ctas == 2) return launch<2, 256, KIND>(maps, a, num_sms, stream);
-  return plan.cols == 256 ? launch<1, 256, KIND>(maps, a, num_sms, stream)
-                          : launch<1, 128, KIND>(maps, a, num_sms, stream);
+cudaError_t launch_plan(const GroupedMaps& maps, const GroupedArgs& a, const GroupedPlan& plan,
+                        cudaStream_t stream) {
+  if (plan.ctas == 2) return launch<2, 256, KIND>(maps, a, plan, stream);
+  if (plan.cols == 256) return launch<1, 256, KIND>(maps, a, plan, stream);
+  return plan.split > 1 ? launch<1, 128, KIND, true>(maps, a, plan, stream)
+                        : launch<1, 128, KIND>(maps, a, plan, stream);
 }
-
-}  // namespace
 
 // The cut with the least estimated time: waves of tiles over the GPU, each so
 // many clocks a stage and so many more, as measured with all SMs at work (128
@@ -924,10 +904,10 @@ cudaError_t launch_plan(GroupedPlan plan, const GroupedMaps& maps, const Grouped
 // 25.6, 21.8 and 25.5 us).  A contraction of four stages or less leaves the
 // epilogue alone to bound the call, and two whole accumulators of 128 columns
 // keep it busiest (weight gradients of 64 experts x 1408 x 2048 from 128 rows
-// each 200, 166 and 147 us).
-GroupedPlan grouped_plan(int64_t rows, int64_t cols, int64_t depth, int groups, bool wgrad,
-                         int num_sms) {
-  if (!wgrad && rows <= static_cast<int64_t>(groups) * FEW_ROWS) return {1, 32, true};
+// each 200, 166 and 147 us).  For groups of rows / groups output rows on average.
+GroupedPlan cut(int64_t rows, int64_t cols, int64_t depth, int64_t groups, bool wgrad,
+                int num_sms) {
+  if (!wgrad && rows <= groups * FEW_ROWS) return {1, 32, true};
   if (depth <= 4 * STEP_K) return {1, 128, false};
   auto clocks = [&](int ctas, int bn, int stage, int fixed) {
     const int64_t tile = ROWS * ctas;
@@ -942,11 +922,37 @@ GroupedPlan grouped_plan(int64_t rows, int64_t cols, int64_t depth, int groups, 
   return {pair <= wide ? 2 : 1, 256, false};
 }
 
+}  // namespace
+
+GroupedPlan grouped_plan(int64_t M, int64_t N, int64_t K, int64_t groups, bool wgrad,
+                         bool out_f32, int num_sms) {
+  GroupedPlan plan = wgrad ? cut(N * groups, K, M / groups, groups, true, num_sms)
+                           : cut(M, N, K, groups, false, num_sms);
+  // At most this many tiles, whatever the offsets are: every group has a row more
+  // than whole tiles.
+  const int64_t used = groups < M ? groups : M;
+  auto ragged = [&](int tile) { return (M - used) / tile + used; };
+  auto whole = [](int64_t n, int tile) { return (n + tile - 1) / tile; };
+  const int tile_m = ROWS * plan.ctas;
+  plan.tiles = wgrad      ? groups * whole(N, tile_m) * whole(K, plan.cols)
+               : plan.few ? ragged(plan.cols) * whole(N, tile_m)
+                          : ragged(tile_m) * whole(N, plan.cols);
+  plan.split = plan.cols == 256 ? 1
+               : wgrad          ? ranges(M / groups, M, plan.tiles, out_f32, num_sms)
+                                : ranges(K, K, plan.tiles, out_f32, num_sms);
+  const int cluster = plan.split > 1 ? plan.split : plan.ctas;
+  const int64_t most = num_sms / cluster;
+  plan.grid = static_cast<int>(plan.tiles < most ? plan.tiles : most) * cluster;
+  return plan;
+}
+
 cudaError_t launch_grouped(const GroupedMaps& maps, const GroupedArgs& a, bool wgrad,
-                           GroupedPlan plan, int num_sms, cudaStream_t stream) {
-  if (plan.few) return launch<1, 32, FEW>(maps, a, num_sms, stream);
-  return wgrad ? launch_plan<WGRAD>(plan, maps, a, num_sms, stream)
-               : launch_plan<FORWARD>(plan, maps, a, num_sms, stream);
+                           const GroupedPlan& plan, cudaStream_t stream) {
+  if (plan.few)
+    return plan.split > 1 ? launch<1, 32, FEW, true>(maps, a, plan, stream)
+                          : launch<1, 32, FEW>(maps, a, plan, stream);
+  return wgrad ? launch_plan<WGRAD>(maps, a, plan, stream)
+               : launch_plan<FORWARD>(maps, a, plan, stream);
 }
 
 }  // namespace mxq

@@ -82,7 +82,8 @@ mxq_status mx_grouped_gemm(const uint8_t* x_q, const uint8_t* x_s, const uint8_t
   a.s_ld = K / 32;
   a.dev_err = dev_err;
   a.timeout_ns = mxq::PRODUCT_TIMEOUT_NS;
-  const mxq::GroupedPlan plan = mxq::grouped_plan(M, N, K, a.groups, false, sms);
+  const mxq::GroupedPlan plan = mxq::grouped_plan(M, N, K, E, false, a.out_f32, sms);
+  a.split = plan.split;
   (plan.few ? a.a_rows : a.b_rows) = static_cast<int>(N);
   a.a_s = plan.few ? w_s : x_s;
   a.b_s = plan.few ? x_s : w_s;
@@ -94,7 +95,7 @@ mxq_status mx_grouped_gemm(const uint8_t* x_q, const uint8_t* x_s, const uint8_t
                       plan.few ? 128 : plan.box_rows());
     if (st != MXQ_OK) return st;
   }
-  return from_cuda(mxq::launch_grouped(maps, a, false, plan, sms, stream));
+  return from_cuda(mxq::launch_grouped(maps, a, false, plan, stream));
 }
 
 mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, const uint8_t* x_q,
@@ -129,14 +130,15 @@ mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, const uint8_
   a.s_ld = M / 32;
   a.dev_err = dev_err;
   a.timeout_ns = mxq::PRODUCT_TIMEOUT_NS;
-  const mxq::GroupedPlan plan = mxq::grouped_plan(N * E, K, M / E, a.groups, true, sms);
+  const mxq::GroupedPlan plan = mxq::grouped_plan(M, N, K, E, true, a.out_f32, sms);
+  a.split = plan.split;
   if (M > 0) {
     st = encode_codes(&maps.a, g_q, 1, N, M, 128);
     if (st != MXQ_OK) return st;
     st = encode_codes(&maps.b, x_q, 1, K, M, plan.box_rows());
     if (st != MXQ_OK) return st;
   }
-  return from_cuda(mxq::launch_grouped(maps, a, true, plan, sms, stream));
+  return from_cuda(mxq::launch_grouped(maps, a, true, plan, stream));
 }
 
 mxq_status nvfp4_gemv(const void* x, int64_t ldx, const uint8_t* w_q, const uint8_t* w_s,
@@ -179,7 +181,40 @@ mxq_status nvfp4_gemv(const void* x, int64_t ldx, const uint8_t* w_q, const uint
   a.out_f32 = size == 4;
   a.dev_err = dev_err;
   a.timeout_ns = mxq::PRODUCT_TIMEOUT_NS;
-  return from_cuda(mxq::launch_nvfp4_gemv(a, sms, stream));
+  const mxq::GemvPlan plan = mxq::gemv_plan(a.rows, N, K, experts ? E : 0, sms);
+  return from_cuda(mxq::launch_nvfp4_gemv(a, plan, stream));
+}
+
+mxq_status mxq_product_plan(int op, int64_t M, int64_t N, int64_t K, int64_t E, uint32_t flags,
+                            int num_sms, int32_t* plan) {
+  if (!plan || num_sms < 1 || (flags & ~static_cast<uint32_t>(MXQ_OUT_F32))) return MXQ_EINVAL;
+  // Without rows a gradient is zeros, and without depth a product.
+  const bool wgrad = op == MXQ_OP_GROUPED_WGRAD;
+  if (M < (wgrad ? 0 : 1) || N < 1 || K < (wgrad ? 1 : 0) || M % (wgrad ? 32 : 1) ||
+      K % (wgrad ? 1 : 32) || M > kMost || N > kMost || K > kMost)
+    return MXQ_ESHAPE;
+  if (wgrad || op == MXQ_OP_GROUPED_GEMM) {
+    if (E < 1 || E > mxq::GROUPS_MAX) return MXQ_ESHAPE;
+    const mxq::GroupedPlan p =
+        mxq::grouped_plan(M, N, K, E, wgrad, (flags & MXQ_OUT_F32) != 0, num_sms);
+    plan[0] = p.ctas;
+    plan[1] = p.cols;
+    plan[2] = p.few;
+    plan[3] = p.split;
+    plan[4] = p.tiles > INT32_MAX ? INT32_MAX : static_cast<int32_t>(p.tiles);
+    plan[5] = p.grid;
+    return MXQ_OK;
+  }
+  if (op != MXQ_OP_NVFP4_GEMV) return MXQ_EINVAL;
+  if (E < 0 || E > mxq::GEMV_EXPERTS_MAX) return MXQ_ESHAPE;
+  const mxq::GemvPlan p = mxq::gemv_plan(M, N, K, E, num_sms);
+  plan[0] = p.toks;
+  plan[1] = p.tiles;
+  plan[2] = p.cluster;
+  plan[3] = p.cap;
+  plan[4] = p.items > INT32_MAX ? INT32_MAX : static_cast<int32_t>(p.items);
+  plan[5] = p.grid;
+  return MXQ_OK;
 }
 
 }  // extern "C"

@@ -29,7 +29,7 @@ struct GroupedArgs {
   int a_rows;               // wgrad, few: N
   int b_rows;               // forward: N; wgrad: K
   int depth;                // forward: K
-  int split;                // CTAs of a cluster that share a tile's contraction (set by the launch)
+  int split;                // GroupedPlan::split
   const uint8_t* a_s;       // E8M0 scales, s_ld bytes a row
   const uint8_t* b_s;
   int64_t s_ld;
@@ -55,15 +55,18 @@ struct GroupedPlan {
   int ctas;
   int cols;
   bool few;                // few rows a group: they are B, and the weight A
+  int split;               // CTAs of a cluster that share a tile's contraction, or 1
+  int64_t tiles;           // at most this many
+  int grid;                // CTAs launched
   int box_rows() const { return cols / ctas; }   // rows of one copy of B
 };
 
-// The plan for groups of rows / groups output rows on average, whose elements
-// are sums of `depth` products.
-GroupedPlan grouped_plan(int64_t rows, int64_t cols, int64_t depth, int groups, bool wgrad,
-                         int num_sms);
+// The plan of mx_grouped_gemm, or of mx_grouped_wgrad, for sizes that are not
+// empty.
+GroupedPlan grouped_plan(int64_t M, int64_t N, int64_t K, int64_t groups, bool wgrad,
+                         bool out_f32, int num_sms);
 cudaError_t launch_grouped(const GroupedMaps& maps, const GroupedArgs& a, bool wgrad,
-                           GroupedPlan plan, int num_sms, cudaStream_t stream);
+                           const GroupedPlan& plan, cudaStream_t stream);
 
 constexpr int GEMV_EXPERTS_MAX = 4096;
 
@@ -84,7 +87,18 @@ struct GemvArgs {
   uint64_t timeout_ns;
 };
 
-cudaError_t launch_nvfp4_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream);
+// How a call is cut: 16 * tiles output columns a CTA, K over clusters, at most
+// `cap` rows of x at a time, by the kernel for up to `toks` (8 or 16).
+struct GemvPlan {
+  int toks;
+  int tiles, cluster, cap;
+  int64_t items;           // experts that may have rows, times their blocks of columns
+  int grid;                // CTAs launched
+};
+
+// The plan for `rows` output rows; experts is 0 for one weight and no ids.
+GemvPlan gemv_plan(int64_t rows, int64_t n, int64_t k, int64_t experts, int num_sms);
+cudaError_t launch_nvfp4_gemv(const GemvArgs& a, const GemvPlan& plan, cudaStream_t stream);
 
 // Host helpers (mxq_api.cu).
 // Allows `kernel` (a __global__ function) `bytes` of dynamic shared memory on the

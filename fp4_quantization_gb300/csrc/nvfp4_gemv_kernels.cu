@@ -622,11 +622,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
   if (!ok && a.dev_err) atomicOr(a.dev_err, MXQ_DEVERR_TIMEOUT);
 }
 
-// How the work is cut: 16 * tiles output columns a CTA, K over clusters, at most
-// `cap` rows of x at a time.
-struct Plan {
-  int tiles, cluster, cap;
-};
+}  // namespace
 
 // One or two rows: of the cuts into 1, 2, 4 or 8 tiles an item, 8, 4, 2 or 1
 // parts of K, the one with the least estimated time.  Few parts mean few copies
@@ -639,17 +635,25 @@ struct Plan {
 // time, so that the staged rows are shared out too (4099 x 11008 weights, thirteen
 // rows: 17.4 us over clusters of 8, 84 in one CTA, 34 in halves; 14336 x 4096, four
 // rows: 18.1, 14.5 and 19.2 us over clusters of 1, 2 and 4).
-Plan choose(const GemvArgs& a, int rows, int toks, int x_bytes, int64_t slots, int num_sms) {
-  const int64_t steps = (a.k + STEP_K - 1) / STEP_K;
-  auto items = [&](int tiles) { return (a.n + tiles * 16 - 1) / (tiles * 16) * slots; };
-  Plan plan{WARPS, 1, a.experts || a.rows > toks ? toks : a.rows};
+GemvPlan gemv_plan(int64_t rows, int64_t n, int64_t k, int64_t experts, int num_sms) {
+  // At most this many experts have rows, and then this many rows each.
+  const int64_t slots = experts == 0 ? 1 : rows < experts ? rows : experts;
+  const int64_t each = (rows + slots - 1) / slots;
+  // With more than 4 rows an expert on average some have more than 8, and would read
+  // their weights twice (7 experts with 52 rows, 16455 x 960: 35 us sixteen rows at a
+  // time, 55 eight; 11 with 36, 4633 x 4608: 90 and 54).
+  const int toks = each > (experts > 0 ? 4 : 8) ? 16 : 8;
+  const int x_bytes = toks == 16 ? Shape<16>::X_BYTES : Shape<8>::X_BYTES;
+  const int64_t steps = (k + STEP_K - 1) / STEP_K;
+  auto items = [&](int tiles) { return (n + tiles * 16 - 1) / (tiles * 16) * slots; };
+  GemvPlan plan{toks, WARPS, 1, experts > 0 || rows > toks ? toks : static_cast<int>(rows)};
   // Quarters of a round of two CTAs an SM; a last one of at most a CTA an SM takes
   // three.
   auto rounds = [&](int64_t n) {
     const int64_t rest = n % (2 * num_sms);
     return n / (2 * num_sms) * 4 + (rest > num_sms ? 4 : rest > 0 ? 3 : 0);
   };
-  if (rows <= 2) {
+  if (each <= 2) {
     // In eighths of a step of all warps, a step more an item.
     auto cost = [&](int tiles) { return rounds(items(tiles)) * (steps * tiles + 8); };
     for (int tiles = WARPS / 2; tiles > 0; tiles /= 2)
@@ -669,19 +673,22 @@ Plan choose(const GemvArgs& a, int rows, int toks, int x_bytes, int64_t slots, i
   // Rows whose range of K is staged whole, if that takes all that are expected.
   const int64_t range = (steps + plan.cluster - 1) / plan.cluster;
   const int64_t fit = x_bytes / (2 * STEP_K) / (range > 0 ? range : 1);
-  if (fit >= rows && fit < plan.cap) plan.cap = static_cast<int>(fit);
+  if (fit >= (each < 16 ? each : 16) && fit < plan.cap) plan.cap = static_cast<int>(fit);
+  plan.items = items(plan.tiles);
+  const int64_t most = 2 * num_sms / plan.cluster;
+  plan.grid = static_cast<int>(plan.items < most ? plan.items : most) * plan.cluster;
   return plan;
 }
 
+namespace {
+
 template <int TOKS>
-cudaError_t launch(const GemvArgs& a, int rows, int64_t slots, int num_sms,
-                   cudaStream_t stream) {
+cudaError_t launch(const GemvArgs& a, const GemvPlan& plan, cudaStream_t stream) {
   constexpr int smem = Shape<TOKS>::SMEM;
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e =
       allow_shared(reinterpret_cast<const void*>(nvfp4_gemv_kernel<TOKS>), smem, &allowed);
   if (e != cudaSuccess) return e;
-  const Plan plan = choose(a, rows, TOKS, Shape<TOKS>::X_BYTES, slots, num_sms);
   // w_q as rows of bytes, a copy of a line each of a CTA's rows.
   CUtensorMap codes{};
   if (a.k > 0) {
@@ -693,10 +700,8 @@ cudaError_t launch(const GemvArgs& a, int rows, int64_t slots, int num_sms,
                    CU_TENSOR_MAP_SWIZZLE_128B) != MXQ_OK)
       return cudaErrorInvalidValue;
   }
-  const int64_t items = (a.n + plan.tiles * 16 - 1) / (plan.tiles * 16) * slots;
-  const int64_t most = 2 * num_sms / plan.cluster;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(items < most ? items : most) * plan.cluster);
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.grid));
   cfg.blockDim = dim3(32 * WARPS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -713,15 +718,8 @@ cudaError_t launch(const GemvArgs& a, int rows, int64_t slots, int num_sms,
 
 }  // namespace
 
-cudaError_t launch_nvfp4_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream) {
-  // At most this many experts have rows, and then this many rows each.
-  const int64_t slots = !a.experts ? 1 : a.rows < a.num_experts ? a.rows : a.num_experts;
-  const int rows = a.experts ? static_cast<int>((a.rows + slots - 1) / slots) : a.rows;
-  // With more than 4 rows an expert on average some have more than 8, and would read
-  // their weights twice (7 experts with 52 rows, 16455 x 960: 35 us sixteen rows at a
-  // time, 55 eight; 11 with 36, 4633 x 4608: 90 and 54).
-  return rows > (a.experts ? 4 : 8) ? launch<16>(a, rows < 16 ? rows : 16, slots, num_sms, stream)
-                                    : launch<8>(a, rows, slots, num_sms, stream);
+cudaError_t launch_nvfp4_gemv(const GemvArgs& a, const GemvPlan& plan, cudaStream_t stream) {
+  return plan.toks == 16 ? launch<16>(a, plan, stream) : launch<8>(a, plan, stream);
 }
 
 }  // namespace mxq

@@ -94,6 +94,9 @@ enum {
 /* operation ids for mxq_workspace_bytes */
 enum { MXQ_OP_ROWCOL = 0, MXQ_OP_NVFP4 = 1, MXQ_OP_DACT = 2, MXQ_OP_ROWCOL_HOST = 3 };
 
+/* operation ids for mxq_product_plan */
+enum { MXQ_OP_GROUPED_GEMM = 4, MXQ_OP_GROUPED_WGRAD = 5, MXQ_OP_NVFP4_GEMV = 6 };
+
 /* Human-readable name of a status code (static string, never NULL). */
 MXQ_API const char* mxq_status_string(int status);
 
@@ -392,6 +395,24 @@ MXQ_API mxq_status nvfp4_gemv(const void* x, int64_t ldx, const uint8_t* w_q, co
                               const float* w_global, const int32_t* experts, int64_t T,
                               int64_t share, int64_t N, int64_t K, int64_t E, uint32_t flags,
                               void* out, int64_t ldo, uint32_t* dev_err, mxq_stream_t stream);
+
+/*
+ * mxq_product_plan -- how a product's call is cut on a GPU of num_sms SMs.  Host
+ * code only: it needs no device, so that tests can name the kernel that a call
+ * takes.
+ *
+ *   MXQ_OP_GROUPED_GEMM, MXQ_OP_GROUPED_WGRAD: the call's M, N, K, E, flags.
+ *   MXQ_OP_NVFP4_GEMV: M = T * share; E = 0 stands for a call without experts.
+ *   plan [6], grouped: CTAs that work on a tile; a tile's columns; 1 where few
+ *           rows a group make the weight the 128-row operand; CTAs that share a
+ *           tile's contraction; tiles at most; CTAs launched.
+ *   plan [6], nvfp4_gemv: rows of the kernel (8 or 16); blocks of 16 columns an
+ *           item; CTAs that share an item's K; rows of x at a time; items at
+ *           most; CTAs launched.
+ * MXQ_ESHAPE for sizes that the call refuses or that make it empty.
+ */
+MXQ_API mxq_status mxq_product_plan(int op, int64_t M, int64_t N, int64_t K, int64_t E,
+                                    uint32_t flags, int num_sms, int32_t* plan);
 
 /*
  * mxq_selftest_bounded_wait -- launches one warp that waits on a barrier
