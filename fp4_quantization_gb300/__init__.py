@@ -443,7 +443,7 @@ def nvfp4_gemv(x, w_q, w_s, global_scale, *, experts=None, share=1, out=None,
 
 _PLAN_FIELDS = {OP_GROUPED_GEMM: ("ctas", "cols", "few", "split", "tiles", "grid"),
                 OP_GROUPED_WGRAD: ("ctas", "cols", "few", "split", "tiles", "grid"),
-                OP_NVFP4_GEMV: ("toks", "tiles", "cluster", "cap", "items", "grid")}
+                OP_NVFP4_GEMV: ("toks", "tiles", "cluster", "cap", "items", "grid", "uneven")}
 
 
 def mxq_product_plan(op, M, N, K, E, flags=0, *, num_sms=None):
@@ -452,7 +452,7 @@ def mxq_product_plan(op, M, N, K, E, flags=0, *, num_sms=None):
     OP_NVFP4_GEMV takes M = T * share, and E = 0 for a call without experts."""
     if num_sms is None:
         num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
-    plan = (ctypes.c_int32 * 6)()
+    plan = (ctypes.c_int32 * 7)()
     _check(_lib.lib().mxq_product_plan(op, M, N, K, E, flags, num_sms, plan), "mxq_product_plan")
     return dict(zip(_PLAN_FIELDS[op], plan))
 

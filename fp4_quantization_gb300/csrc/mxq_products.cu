@@ -203,6 +203,7 @@ mxq_status mxq_product_plan(int op, int64_t M, int64_t N, int64_t K, int64_t E, 
     plan[3] = p.split;
     plan[4] = p.tiles > INT32_MAX ? INT32_MAX : static_cast<int32_t>(p.tiles);
     plan[5] = p.grid;
+    plan[6] = 0;
     return MXQ_OK;
   }
   if (op != MXQ_OP_NVFP4_GEMV) return MXQ_EINVAL;
@@ -214,6 +215,7 @@ mxq_status mxq_product_plan(int op, int64_t M, int64_t N, int64_t K, int64_t E, 
   plan[3] = p.cap;
   plan[4] = p.items > INT32_MAX ? INT32_MAX : static_cast<int32_t>(p.items);
   plan[5] = p.grid;
+  plan[6] = p.uneven;
   return MXQ_OK;
 }
 

@@ -92,6 +92,7 @@ struct GemvArgs {
 struct GemvPlan {
   int toks;
   int tiles, cluster, cap;
+  bool uneven;             // how much of K is staged follows each expert's rows
   int64_t items;           // experts that may have rows, times their blocks of columns
   int grid;                // CTAs launched
 };

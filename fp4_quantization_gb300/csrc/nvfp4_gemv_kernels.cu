@@ -149,7 +149,11 @@ __device__ __forceinline__ void multiply_step(float (&acc)[2][Shape<TOKS>::TILES
 // turn); a cluster's CTAs split K into ranges.  The parts leave their sums in
 // shared memory; when its places are full, or the rows of x change, they are
 // added in a fixed order, and those of a cluster's CTAs by its first one.
-template <int TOKS>
+//
+// K is staged in chunks of what fits of the rows: of `cap`, or with UNEVEN of those
+// that the pass has, so that an expert with few rows keeps them staged while another
+// with many takes them in one pass over its weights.
+template <int TOKS, bool UNEVEN>
 __global__ void __launch_bounds__(32 * WARPS, 2)
 nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, const int tiles,
                   const int cluster, const int cap) {
@@ -162,10 +166,12 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
   __shared__ uint32_t present[GEMV_EXPERTS_MAX / 32];
   __shared__ uint16_t active[GEMV_EXPERTS_MAX];           // the experts that have rows
   __shared__ int warp_sum[WARPS];
-  __shared__ int list[TOKS + 2];                          // rows of the expert, their number, the next
+  // Rows of the expert, their number, the next; whether its first room is another.
+  __shared__ int list[TOKS + 3];
   __shared__ uint32_t extent[TILES * WARPS];               // of a warp's share of a row of x
   __shared__ uint64_t full[WARPS][DEPTH], empty[WARPS][DEPTH];   // of a part's places
   __shared__ uint4 zeros[1];
+  __shared__ int rooms[2];                                // UNEVEN: of this pass, of its expert's first
   __shared__ float2 unit[TOKS];                           // what a sum of staged row i is multiplied by
   const int tid = threadIdx.x, lane = tid % 32, g = lane / 4, t = lane % 4;
   const int warp = __shfl_sync(~0u, tid / 32, 0);          // the same for the warp, known to be
@@ -227,9 +233,10 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
     const int nth = a.experts ? i / groups : 0;
     return Item{a.experts ? static_cast<int>(active[nth]) : 0, (i - nth * groups) * tiles * 16};
   };
-  // K is staged in chunks of `room` at most (one, unless rows and K are both
-  // large); a warp's steps in the chunk from k0 on start at start_of(k0).
-  const int room = S::X_BYTES / (cap * 2) / STEP_K * STEP_K;
+  // A warp's steps in the chunk from k0 on start at start_of(k0).
+  auto room_for = [&](int rows) { return S::X_BYTES / (rows * 2) / STEP_K * STEP_K; };
+  const int even = room_for(cap);
+  auto room_of = [&](int i) { return UNEVEN ? rooms[i] : even; };
   const int turn = parts * STEP_K;
   auto start_of = [&](int k0) {
     const int behind = (k0 - k_first - part * STEP_K) % turn;
@@ -249,6 +256,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
     fence_barrier_init();
   }
   if (tid == 0) zeros[0] = make_uint4(0, 0, 0, 0);
+  if (UNEVEN && tid < 2) rooms[tid] = even;
   __syncthreads();
   const bool words = a.k % 64 == 0;                   // rows of scales start on 4 bytes
   const uint8_t* s[2] = {};                           // this thread's scales at k = 0
@@ -258,7 +266,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
   bool ok = true;                                     // no wait of the warp ran out
   const int whole_to = words ? a.k - STEP_K : -1;     // a step from here has all its scales
   int load_end = 0;
-  auto load_start = [&] {
+  auto load_start = [&](int room) {
     load_k = start_of(load_k0);
     load_end = load_item < item_end ? min(load_k0 + room, k_end) : 0;
     if (load_item >= item_end) return;
@@ -270,7 +278,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
       s[h] = a.w_s + (static_cast<int64_t>(item.e) * a.n + min(n + g + 8 * h, a.n - 1)) * (a.k / 16) +
              4 * t;
   };
-  auto load_next = [&](int i, uint32_t (&v)[2][2]) {
+  auto load_next = [&](int i, uint32_t (&v)[2][2], int item) {
     if (ok && load_k < load_end) {
       if (tile == 0) {
         // The place has been read by all the part's warps.
@@ -303,12 +311,14 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
     }
     load_k += turn;
     if (i == DEPTH - 1 && load_k >= load_end) {
-      load_k0 += room;
+      // The loads can be two short chunks ahead, and so have to leave one of an item
+      // after this one's, whose expert's rows are not known yet.
+      load_k0 += room_of(load_item != item);
       if (load_k0 >= k_end) {
         load_k0 = k_first;
         ++load_item;
       }
-      load_start();
+      load_start(room_of(load_item != item));
     }
   };
   auto wait_for = [&](int i) {
@@ -351,11 +361,19 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
       if (lane == 0) {
         list[TOKS] = have;
         list[TOKS + 1] = at;
+        if constexpr (UNEVEN) {
+          const int room = min(room_for(have), max(range, 1) * STEP_K);
+          list[TOKS + 2] = from == 0 && rooms[1] != room;
+          rooms[0] = room;
+          if (from == 0) rooms[1] = room;
+        }
       }
     }
     __syncthreads();
     found = list[TOKS];
     next_row = list[TOKS + 1];
+    // What the loads hold was cut to the last expert's chunks.
+    if (UNEVEN && list[TOKS + 2]) held_item = -1;
   };
   auto row_at = [&](int m) { return a.experts ? list[m] : row0 + m; };
 
@@ -519,6 +537,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
     const float global = a.w_global[here.e];
     while (true) {
       const int rows = found, after = next_row;
+      const int room = room_of(0);
       float out[TILES][4] = {};
       for (int k0 = k_first; k0 < k_end; k0 += room) {
         const int k1 = min(k0 + room, k_end);
@@ -544,7 +563,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
               }
             load_item = item;
             load_k0 = k0;
-            load_start();
+            load_start(room);
           }
           int k = start_of(k0);
           // This thread's pieces of x at k = k0.
@@ -573,7 +592,7 @@ nvfp4_gemv_kernel(const __grid_constant__ CUtensorMap codes, const GemvArgs a, c
                                     g, t);
                 release(i);
               }
-              load_next(i, scale[i]);
+              load_next(i, scale[i], item);
               if (!fill) k += turn;
             }
 #pragma unroll
@@ -646,7 +665,7 @@ GemvPlan gemv_plan(int64_t rows, int64_t n, int64_t k, int64_t experts, int num_
   const int x_bytes = toks == 16 ? Shape<16>::X_BYTES : Shape<8>::X_BYTES;
   const int64_t steps = (k + STEP_K - 1) / STEP_K;
   auto items = [&](int tiles) { return (n + tiles * 16 - 1) / (tiles * 16) * slots; };
-  GemvPlan plan{toks, WARPS, 1, experts > 0 || rows > toks ? toks : static_cast<int>(rows)};
+  GemvPlan plan{toks, WARPS, 1, experts > 0 || rows > toks ? toks : static_cast<int>(rows), false};
   // Quarters of a round of two CTAs an SM; a last one of at most a CTA an SM takes
   // three.
   auto rounds = [&](int64_t n) {
@@ -670,10 +689,18 @@ GemvPlan gemv_plan(int64_t rows, int64_t n, int64_t k, int64_t experts, int num_
       if (cost(cluster) <= cost(plan.cluster)) plan.cluster = cluster;
   }
   while (plan.tiles > 1 && items(plan.tiles) * plan.cluster < num_sms / 2) plan.tiles /= 2;
-  // Rows whose range of K is staged whole, if that takes all that are expected.
+  // Rows whose range of K is staged whole.  An expert with more than `cap` has its
+  // weights read again, and how many one has is not known here: where a quarter of
+  // the kernel's rows would be lost, the room follows each expert's rows instead (128
+  // rows over 64 experts, 4096 x 7168, where 2 fit: 440 us two at a time, 210 so).
+  // That costs ordinary calls a little (32 rows over 64 experts, 2816 x 2048, 7 fit:
+  // 25.3 us seven at a time, 25.9 so).
   const int64_t range = (steps + plan.cluster - 1) / plan.cluster;
   const int64_t fit = x_bytes / (2 * STEP_K) / (range > 0 ? range : 1);
-  if (fit >= (each < 16 ? each : 16) && fit < plan.cap) plan.cap = static_cast<int>(fit);
+  if (experts > 0 && fit < toks) {
+    plan.uneven = 4 * fit < 3 * toks;
+    if (!plan.uneven) plan.cap = static_cast<int>(fit);
+  }
   plan.items = items(plan.tiles);
   const int64_t most = 2 * num_sms / plan.cluster;
   plan.grid = static_cast<int>(plan.items < most ? plan.items : most) * plan.cluster;
@@ -682,12 +709,12 @@ GemvPlan gemv_plan(int64_t rows, int64_t n, int64_t k, int64_t experts, int num_
 
 namespace {
 
-template <int TOKS>
+template <int TOKS, bool UNEVEN>
 cudaError_t launch(const GemvArgs& a, const GemvPlan& plan, cudaStream_t stream) {
   constexpr int smem = Shape<TOKS>::SMEM;
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e =
-      allow_shared(reinterpret_cast<const void*>(nvfp4_gemv_kernel<TOKS>), smem, &allowed);
+  auto kernel = nvfp4_gemv_kernel<TOKS, UNEVEN>;
+  const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), smem, &allowed);
   if (e != cudaSuccess) return e;
   // w_q as rows of bytes, a copy of a line each of a CTA's rows.
   CUtensorMap codes{};
@@ -712,14 +739,15 @@ cudaError_t launch(const GemvArgs& a, const GemvPlan& plan, cudaStream_t stream)
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, nvfp4_gemv_kernel<TOKS>, codes, a, plan.tiles, plan.cluster,
-                            plan.cap);
+  return cudaLaunchKernelEx(&cfg, kernel, codes, a, plan.tiles, plan.cluster, plan.cap);
 }
 
 }  // namespace
 
 cudaError_t launch_nvfp4_gemv(const GemvArgs& a, const GemvPlan& plan, cudaStream_t stream) {
-  return plan.toks == 16 ? launch<16>(a, plan, stream) : launch<8>(a, plan, stream);
+  if (plan.uneven)
+    return plan.toks == 16 ? launch<16, true>(a, plan, stream) : launch<8, true>(a, plan, stream);
+  return plan.toks == 16 ? launch<16, false>(a, plan, stream) : launch<8, false>(a, plan, stream);
 }
 
 }  // namespace mxq

@@ -388,8 +388,10 @@ MXQ_API mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, cons
  *           or >= E is zero (it belongs to another rank, or to no token).
  *           NULL: one weight (E == 1, share == 1).
  *   out     [T * share][ldo].
- * Meant for up to 16 rows of each expert; more are right, and read the
- * weights once for every 16.
+ * Meant for up to 16 rows of each expert; more are right.  The weights are read
+ * once for every 16 rows; with experts, an expert's once for every 12 of its rows
+ * at least, or every 6 where T * share is at most 4 times the smaller of E and
+ * T * share.
  */
 MXQ_API mxq_status nvfp4_gemv(const void* x, int64_t ldx, const uint8_t* w_q, const uint8_t* w_s,
                               const float* w_global, const int32_t* experts, int64_t T,
@@ -403,12 +405,13 @@ MXQ_API mxq_status nvfp4_gemv(const void* x, int64_t ldx, const uint8_t* w_q, co
  *
  *   MXQ_OP_GROUPED_GEMM, MXQ_OP_GROUPED_WGRAD: the call's M, N, K, E, flags.
  *   MXQ_OP_NVFP4_GEMV: M = T * share; E = 0 stands for a call without experts.
- *   plan [6], grouped: CTAs that work on a tile; a tile's columns; 1 where few
+ *   plan [7], grouped: CTAs that work on a tile; a tile's columns; 1 where few
  *           rows a group make the weight the 128-row operand; CTAs that share a
- *           tile's contraction; tiles at most; CTAs launched.
- *   plan [6], nvfp4_gemv: rows of the kernel (8 or 16); blocks of 16 columns an
+ *           tile's contraction; tiles at most; CTAs launched; 0.
+ *   plan [7], nvfp4_gemv: rows of the kernel (8 or 16); blocks of 16 columns an
  *           item; CTAs that share an item's K; rows of x at a time; items at
- *           most; CTAs launched.
+ *           most; CTAs launched; 1 where how much of K is staged follows each
+ *           expert's rows.
  * MXQ_ESHAPE for sizes that the call refuses or that make it empty.
  */
 MXQ_API mxq_status mxq_product_plan(int op, int64_t M, int64_t N, int64_t K, int64_t E,

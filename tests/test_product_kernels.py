@@ -98,10 +98,15 @@ ROUTED_KERNELS = [
     ("items_chunks_skewed", 8, True, True, 8, 16, 2, 7000, 4096, "skewed"),
     ("cluster_chunks", 8, True, True, 8, 16, 2, 6000, 8192, "even"),
     ("cluster_chunks_skewed", 8, True, True, 8, 16, 2, 6000, 8192, "skewed"),
+    ("uneven_chunks", 8, True, True, 64, 16, 8, 600, 7168, "even"),
+    ("uneven_chunks_skewed", 8, True, True, 64, 16, 8, 600, 7168, "skewed"),
+    ("long_chunks_skewed", 8, True, True, 64, 9, 7, 640, 14336, "skewed"),
     ("items", 8, True, False, 40, 12, 4, 1500, 512, "even"),
     ("items_skewed", 8, True, False, 40, 12, 4, 1500, 512, "skewed"),
-    ("sixteen_items_chunks", 16, True, True, 3, 20, 2, 13100, 1600, "even"),
-    ("sixteen_skewed", 16, True, True, 3, 40, 2, 13100, 1600, "skewed"),
+    ("sixteen_items", 16, True, False, 3, 20, 2, 13100, 1600, "even"),
+    ("sixteen_items_skewed", 16, True, False, 3, 40, 2, 13100, 1600, "skewed"),
+    ("sixteen_items_chunks", 16, True, True, 3, 20, 2, 13100, 2400, "even"),
+    ("sixteen_chunks_skewed", 16, True, True, 12, 45, 3, 3500, 2400, "skewed"),
     ("experts_1500", 8, True, False, 1500, 100, 4, 130, 64, "even"),
     ("experts_4096", 8, True, False, 4096, 300, 8, 24, 96, "even"),
     ("experts_4096_skewed", 8, True, False, 4096, 64, 8, 24, 96, "skewed"),
@@ -159,8 +164,19 @@ def test_the_gemv_cases_reach_every_way():
              [(c[0], c[1], c[2], 0) for c in GEMV] + [(c[4], c[5], c[6], 0) for c in GEMV_KERNELS]
              + [(c[1] * c[2], c[3], c[4], c[0]) for c in ROUTED]
              + [(c[5] * c[6], c[7], c[8], c[4]) for c in ROUTED_KERNELS]]
+    assert {(p["toks"], p["uneven"]) for p in plans} == {(t, u) for t in (8, 16) for u in (0, 1)}
     assert {(p["toks"], p["cluster"]) for p in plans} >= {(t, c) for t in (8, 16) for c in (1, 2, 8)}
     assert {p["tiles"] for p in plans} == {1, 2, 4, 8}
+
+
+@pytest.mark.parametrize("E,T,share,N,K", [(64, 16, 8, 4096, 7168), (64, 8, 8, 4096, 14336),
+                                           (8, 16, 2, 6000, 6144), (64, 8, 4, 2816, 2048),
+                                           (128, 16, 1, 2048, 28672)])
+def test_routed_rows_share_a_pass(E, T, share, N, K):
+    """Each pass over an expert's rows reads its weights, so that a pass takes three
+    quarters at least of the rows that the kernel multiplies, however long K is."""
+    p = mxq.mxq_product_plan(mxq.OP_NVFP4_GEMV, T * share, N, K, E, num_sms=SMS)
+    assert 4 * p["cap"] >= 3 * p["toks"]
 
 
 def test_plan_refusals():
