@@ -370,7 +370,9 @@ def mx_grouped_gemm(x_q, x_s, w_q, w_s, offsets, *, out=None, out_dtype=torch.bf
     [M,K/32] and w_q [E,N,K] / w_s [E,N,K/32] as mx_quantize_rowcol writes
     them (ROWWISE, row-major scales), offsets [E+1] int32; returns [M,N]
     bf16 or fp32.  Rows in no group are not written.  For the input gradient
-    pass the gradient's rows and the weights' COLWISE codes [E,K,N]."""
+    pass the gradient's rows and the weights' COLWISE codes [E,K,N].  fp32
+    outputs are exact to 2^-20 of their norm: the tensor cores cut sums off
+    (include/mxq.h)."""
     M, K = _operand(x_q, "x_q", 2)
     E, N, Kw = _operand(w_q, "w_q", 3)
     if Kw != K or _operand(x_s, "x_s", 2) != (M, K // 32) \
@@ -391,7 +393,7 @@ def mx_grouped_wgrad(g_q, g_s, x_q, x_s, offsets, *, out=None, out_dtype=torch.f
     """The weights' gradients of mx_grouped_gemm: g_q [N,M] / g_s [N,M/32]
     and x_q [K,M] / x_s [K,M/32] as mx_quantize_rowcol writes them
     (COLWISE), offsets [E+1] int32, multiples of 32; returns [E,N,K] fp32 or
-    bf16."""
+    bf16, exact as mx_grouped_gemm's."""
     N, M = _operand(g_q, "g_q", 2)
     K, Mx = _operand(x_q, "x_q", 2)
     if Mx != M or _operand(g_s, "g_s", 2) != (N, M // 32) \

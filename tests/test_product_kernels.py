@@ -273,6 +273,44 @@ def test_large_kernels_keep_nan_where_it_is():
         check(dw[e], g[:, a:b] @ x[:, a:b].t(), None, True)
 
 
+def normal_operand(gen, *shape):
+    """Codes and scales of normal values, as the library quantizes them."""
+    K, rows = shape[-1], torch.Size(shape[:-1]).numel()
+    x = torch.randn(-(-rows // 32) * 32, K, generator=gen, device="cuda").bfloat16()
+    d = mxq.mx_quantize_rowcol(x, mxq.ROWWISE)
+    return d["q_row"][:rows].view(shape), d["s_row"][:rows].view(*shape[:-1], K // 32)
+
+
+@gpu
+@pytest.mark.parametrize("sizes,N,K", [([700], 1904, 1056), ([300, 400], 1904, 8192), ([130, 170], 1904, 8192),
+                                       ([1200, 800], 1600, 8192 + 512), ([16, 5], 4800, 14336),
+                                       ([60], 513, 28672), ([700, 3, 890], 1504, 3 * 8192)])
+def test_fp32_sums_keep_the_documented_error(sizes, N, K):
+    """The errors of fp32 outputs stay below 2^-20 of their norm, in every kernel
+    and however long the sums are: they are taken apart before the tensor cores
+    have cut off more than that."""
+    gen = generator(K + N)
+    M, E = sum(sizes), len(sizes)
+    x_q, x_s = normal_operand(gen, M, K)
+    w_q, w_s = normal_operand(gen, E, N, K)
+    off = offsets_of(sizes)
+    y = mxq.mx_grouped_gemm(x_q, x_s, w_q, w_s, off, out_dtype=torch.float32).double()
+    x, w = mx_values(x_q, x_s), mx_values(w_q, w_s)
+    want = torch.cat([x[a:b] @ w[e].t() for e, (a, b) in enumerate(zip(off[:-1].tolist(), off[1:].tolist()))])
+    assert (y - want).norm() <= 2.0 ** -20 * want.norm()
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(8192, 2048, 1024), (16384, 1100, 2000), (24576, 512, 512), (9600, 2048, 2304)])
+def test_fp32_gradients_keep_the_documented_error(M, N, K):
+    gen = generator(M + N)
+    g_q, g_s = normal_operand(gen, N, M)
+    x_q, x_s = normal_operand(gen, K, M)
+    dw = mxq.mx_grouped_wgrad(g_q, g_s, x_q, x_s, offsets_of([M])).double()
+    want = mx_values(g_q, g_s) @ mx_values(x_q, x_s).t()
+    assert (dw[0] - want).norm() <= 2.0 ** -20 * want.norm()
+
+
 @gpu
 @pytest.mark.parametrize("exact", [True, False], ids=["exact", "random"])
 def test_most_groups(exact):
