@@ -350,8 +350,13 @@ MXQ_API mxq_status nvfp4_quantize_transpose(const void* x, int64_t M, int64_t K,
  * K = 1056, 2^-21.7 at 4096, 2^-20.5 from 8192 on, since longer sums are taken
  * apart and added in fp32; of rounded additions 2^-24.4, 2^-23.3 and 2^-22.7).  A
  * bf16 output's sums are not taken apart; its rounding is larger.
- * Results do not depend on how the rows fall into tiles: an element is always
- * summed in the order of k.
+ * Order: an element is the sum of 1, 2 or 4 ranges of k, each summed in the order
+ * of k and added in order.  How many follows from M, N, K, E, the output's type
+ * and the GPU's SMs (plan[3] of mxq_product_plan: few tiles share their
+ * contraction), and with K it alone decides the bits: where the rows lie, which
+ * kernel takes them and what else a call holds do not.  So the same call gives the
+ * same bits, but a row in a batch of 8 may differ from itself in a batch of 4096
+ * by the errors above.
  */
 MXQ_API mxq_status mx_grouped_gemm(const uint8_t* x_q, const uint8_t* x_s, const uint8_t* w_q,
                                    const uint8_t* w_s, const int32_t* offsets, int64_t M,
@@ -372,6 +377,8 @@ MXQ_API mxq_status mx_grouped_gemm(const uint8_t* x_q, const uint8_t* x_s, const
  *           has one scale, so no group may start or end inside one: pad
  *           groups with zero rows).
  *   dw      [E][N][K], every element written (zeros for an empty group).
+ * Order: as in mx_grouped_gemm.  Ranges end on multiples of 128 of the buffer's
+ * rows, so that a group's bits also depend on where it starts, modulo 128.
  */
 MXQ_API mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, const uint8_t* x_q,
                                     const uint8_t* x_s, const int32_t* offsets, int64_t M,
@@ -400,6 +407,8 @@ MXQ_API mxq_status mx_grouped_wgrad(const uint8_t* g_q, const uint8_t* g_s, cons
  * once for every 16 rows; with experts, an expert's once for every 12 of its rows
  * at least, or every 6 where T * share is at most 4 times the smaller of E and
  * T * share.
+ * Order: fixed, so that the same call gives the same bits.  How a sum is grouped
+ * follows from the sizes, the GPU's SMs and how many rows an expert has.
  */
 MXQ_API mxq_status nvfp4_gemv(const void* x, int64_t ldx, const uint8_t* w_q, const uint8_t* w_s,
                               const float* w_global, const int32_t* experts, int64_t T,

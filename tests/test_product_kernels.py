@@ -312,6 +312,58 @@ def test_fp32_gradients_keep_the_documented_error(M, N, K):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("K", [1056, 4096, 8192 + 512])
+def test_bits_follow_from_the_shared_contraction(K, dtype):
+    """A row's bits are the same in calls of any size, from any kernel, as long as
+    as many CTAs share a tile's contraction."""
+    gen = generator(K)
+    flags = mxq.OUT_F32 if dtype == torch.float32 else 0
+    x_q, x_s = normal_operand(gen, 2500, K)
+    w_q, w_s = normal_operand(gen, 2, 9600, K)
+    seen, kernels = {}, set()
+    for N in (1504, 9600):
+        for sizes in ([7], [32], [33], [300], [700], [1300], [2500], [1200, 1300], [7, 0], [64, 900]):
+            M, E = sum(sizes), len(sizes)
+            plan = gemm_cut(sizes, N, K, 0, 0, flags, sms_here())
+            y = mxq.mx_grouped_gemm(x_q[:M], x_s[:M], w_q[:E, :N].contiguous(), w_s[:E, :N].contiguous(),
+                                    offsets_of(sizes), out_dtype=dtype)
+            kernels.add(plan)
+            first = seen.setdefault(plan[3], y[:7, :1504].clone())
+            assert torch.equal(y[:7, :1504], first), (N, sizes, plan)
+    assert {k[3] for k in kernels} == ({1} if K == 1056 else {1, 2, 4})
+    assert len({k[:3] for k in kernels}) >= 3
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_gradient_bits_follow_from_the_shared_contraction(dtype):
+    gen = generator(31)
+    flags = mxq.OUT_F32 if dtype == torch.float32 else 0
+    rows = 9 * 1024 + 32
+    g_q, g_s = normal_operand(gen, 2048, rows)
+    x_q, x_s = normal_operand(gen, 2304, rows)
+
+    def at(t, before, after, n, unit):
+        """The first n rows of an operand, its group `before` rows into the buffer."""
+        side = torch.zeros(n, before // unit + t.shape[1] + after // unit, dtype=torch.uint8, device="cuda")
+        side[:, before // unit:before // unit + t.shape[1]] = t[:n]
+        return side
+
+    seen, kernels = {}, set()
+    for N, K in ((256, 128), (512, 512), (1100, 1100), (2048, 2304)):
+        for before, after in ((0, 0), (128, 32), (1024, 416)):
+            plan = wgrad_cut([rows], N, K, before, after, flags, sms_here())
+            kernels.add(plan)
+            dw = mxq.mx_grouped_wgrad(at(g_q, before, after, N, 1), at(g_s, before, after, N, 32),
+                                      at(x_q, before, after, K, 1), at(x_s, before, after, K, 32),
+                                      offsets_of([rows], before), out_dtype=dtype)
+            first = seen.setdefault(plan[3], dw[0, :256, :128].clone())
+            assert torch.equal(dw[0, :256, :128], first), (N, K, before, plan)
+    assert {k[3] for k in kernels} >= {1, 4} and len({k[:3] for k in kernels}) >= 2
+
+
+@gpu
 @pytest.mark.parametrize("exact", [True, False], ids=["exact", "random"])
 def test_most_groups(exact):
     """The limit of 512 groups, uneven, some empty."""
@@ -338,6 +390,19 @@ def test_gemv_kernels(name, toks, items, chunks, T, N, K, kind):
         y = mxq.nvfp4_gemv(x, q[0], s[0], g, out_dtype=dtype, dev_err=err)
         assert err.item() == 0
         check(y, want, bound, kind == "exact", name)
+
+
+@gpu
+@pytest.mark.parametrize("E,T,share,N,K", [(0, 13, 1, 4099, 11008), (0, 1, 1, 2048, 2048), (64, 16, 8, 600, 7168)])
+def test_gemv_gives_the_same_bits(E, T, share, N, K):
+    gen = generator(33)
+    x = nv_rows(gen, False, T, K)
+    q, s, g = nv_operand(gen, False, max(E, 1), N, K)
+    ids = draw_ids(gen, "skewed", T * share, E) if E else None
+    call = lambda: mxq.nvfp4_gemv(x, *((q, s, g) if E else (q[0], s[0], g)), experts=ids, share=share,  # noqa: E731
+                                  out_dtype=torch.float32)
+    first = call()
+    assert all(torch.equal(call(), first) for _ in range(20))
 
 
 def draw_ids(gen, how, rows, E):
