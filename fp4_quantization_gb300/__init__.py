@@ -7,6 +7,12 @@ caller does not pass them, pass raw device pointers and the current CUDA
 stream, and raise ``MxqError`` on a non-zero status.  Every step of the
 quantization runs in the library's kernels; there is no fallback path, and
 importing this package fails if libmxq.so cannot be loaded.
+
+No call synchronises, so that what goes wrong on the GPU (a wait that ran out,
+group offsets that are out of order) is only seen in ``dev_err``, a zeroed
+[1] int32 CUDA tensor that the caller passes and reads.  With ``stream``, an
+output that is not passed in is still allocated on the current stream: order
+the one after the other.
 """
 import ctypes
 
@@ -334,6 +340,22 @@ def _operand(t, name, dim, dtype=_U8):
     raise ValueError(f"{name} must be contiguous")
 
 
+_several = None        # whether there is more than one CUDA device, once it is known
+
+
+def _one_device(*tensors):
+    """Every tensor lies on the current device, to which the launch goes.  With one
+    device there is no other, and the calls do not come here (it is 1 us a call)."""
+    global _several
+    if _several is None:
+        _several = torch.cuda.device_count() > 1
+    if _several:
+        found = {t.get_device() for t in tensors if isinstance(t, torch.Tensor)}
+        found.add(torch.cuda.current_device())
+        if len(found) > 1:
+            raise ValueError(f"operands, output and current device differ: devices {sorted(found)}")
+
+
 def _product_out(out, shape, out_dtype, like):
     """The output tensor (allocated when not given), its row stride and the
     flags of its type."""
@@ -342,6 +364,8 @@ def _product_out(out, shape, out_dtype, like):
         if flags is None:
             raise TypeError("the output type is torch.bfloat16 or torch.float32")
         return torch.empty(shape, dtype=out_dtype, device=like.device), max(shape[-1], 1), flags
+    if not isinstance(out, torch.Tensor):
+        raise TypeError("out must be a tensor")
     if tuple(out.shape) != shape or not out.is_cuda:
         raise ValueError(f"out must be a CUDA tensor of shape {shape}")
     if out.dtype not in _OUT_FLAGS:
@@ -352,7 +376,12 @@ def _product_out(out, shape, out_dtype, like):
 
 
 def _err_ptr(dev_err):
-    return None if dev_err is None else dev_err.data_ptr()
+    if dev_err is None:
+        return None
+    if not isinstance(dev_err, torch.Tensor) or not dev_err.is_cuda \
+            or dev_err.element_size() != 4 or dev_err.numel() < 1:
+        raise TypeError("dev_err must be a [1] int32 CUDA tensor")
+    return dev_err.data_ptr()
 
 
 def _raw_stream(stream, like):
@@ -372,7 +401,9 @@ def mx_grouped_gemm(x_q, x_s, w_q, w_s, offsets, *, out=None, out_dtype=torch.bf
     bf16 or fp32.  Rows in no group are not written.  For the input gradient
     pass the gradient's rows and the weights' COLWISE codes [E,K,N].  fp32
     outputs are exact to 2^-20 of their norm: the tensor cores cut sums off
-    (include/mxq.h)."""
+    (include/mxq.h).  Offsets that decrease or leave [0, M] set DEVERR_OFFSETS
+    in dev_err and nothing is written: an output allocated here then holds
+    whatever its memory held."""
     M, K = _operand(x_q, "x_q", 2)
     E, N, Kw = _operand(w_q, "w_q", 3)
     if Kw != K or _operand(x_s, "x_s", 2) != (M, K // 32) \
@@ -381,6 +412,8 @@ def mx_grouped_gemm(x_q, x_s, w_q, w_s, offsets, *, out=None, out_dtype=torch.bf
     if _operand(offsets, "offsets", 1, _I32) != (E + 1,):
         raise ValueError("offsets must have one entry more than there are experts")
     out, ldo, flags = _product_out(out, (M, N), out_dtype, x_q)
+    if _several is not False:
+        _one_device(x_q, x_s, w_q, w_s, offsets, out, dev_err)
     st = _lib.lib().mx_grouped_gemm(
         x_q.data_ptr(), x_s.data_ptr(), w_q.data_ptr(), w_s.data_ptr(), offsets.data_ptr(), M, N,
         K, E, flags, out.data_ptr(), ldo, _err_ptr(dev_err), _raw_stream(stream, x_q))
@@ -393,7 +426,8 @@ def mx_grouped_wgrad(g_q, g_s, x_q, x_s, offsets, *, out=None, out_dtype=torch.f
     """The weights' gradients of mx_grouped_gemm: g_q [N,M] / g_s [N,M/32]
     and x_q [K,M] / x_s [K,M/32] as mx_quantize_rowcol writes them
     (COLWISE), offsets [E+1] int32, multiples of 32; returns [E,N,K] fp32 or
-    bf16, exact as mx_grouped_gemm's."""
+    bf16, exact as mx_grouped_gemm's.  Offsets that break this set
+    DEVERR_OFFSETS in dev_err and nothing is written, as there."""
     N, M = _operand(g_q, "g_q", 2)
     K, Mx = _operand(x_q, "x_q", 2)
     if Mx != M or _operand(g_s, "g_s", 2) != (N, M // 32) \
@@ -405,6 +439,8 @@ def mx_grouped_wgrad(g_q, g_s, x_q, x_s, offsets, *, out=None, out_dtype=torch.f
     out, _, flags = _product_out(out, (E, N, K), out_dtype, g_q)
     if not out.is_contiguous():
         raise ValueError("out must be contiguous")
+    if _several is not False:
+        _one_device(g_q, g_s, x_q, x_s, offsets, out, dev_err)
     st = _lib.lib().mx_grouped_wgrad(
         g_q.data_ptr(), g_s.data_ptr(), x_q.data_ptr(), x_s.data_ptr(), offsets.data_ptr(), M, N,
         K, E, flags, out.data_ptr(), _err_ptr(dev_err), _raw_stream(stream, g_q))
@@ -427,15 +463,17 @@ def nvfp4_gemv(x, w_q, w_s, global_scale, *, experts=None, share=1, out=None,
         N = _operand(w_q, "w_q", 2)[0]
     else:
         E, N, _ = _operand(w_q, "w_q", 3)
-        lead, ids = (E,), experts.data_ptr()
         if _operand(experts, "experts", 1, _I32) != (T * share,):
             raise ValueError("experts must have T * share entries")
+        lead, ids = (E,), experts.data_ptr()
     if K % 2 or w_q.shape != lead + (N, K // 2) \
             or _operand(w_s, "w_s", len(lead) + 2) != lead + (N, K // 16):
         raise ValueError("x [T,K], w_q [(E,) N,K/2] and w_s [(E,) N,K/16] do not agree")
     if _operand(global_scale, "global_scale", 1, _F32) != (E,):
         raise ValueError("global_scale must have one entry for each expert")
     out, ldo, flags = _product_out(out, (T * share, N), out_dtype, x)
+    if _several is not False:
+        _one_device(x, w_q, w_s, global_scale, experts, out, dev_err)
     st = _lib.lib().nvfp4_gemv(
         x.data_ptr(), ldx, w_q.data_ptr(), w_s.data_ptr(), global_scale.data_ptr(), ids, T, share,
         N, K, E, flags, out.data_ptr(), ldo, _err_ptr(dev_err), _raw_stream(stream, x))

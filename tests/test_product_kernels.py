@@ -194,6 +194,81 @@ def test_plan_refusals():
         assert e.value.status == 1
 
 
+class OnDevice(torch.Tensor):
+    """A host tensor that says it lies on a CUDA device (index `at`)."""
+
+    is_cuda = property(lambda self: self.at >= 0)
+
+    def get_device(self):
+        return self.at
+
+
+def on(at, *shape, dtype=torch.uint8):
+    t = torch.zeros(*shape, dtype=dtype).as_subclass(OnDevice)
+    t.at = at
+    return t
+
+
+def product_calls():
+    """Each product's operands by name, with a call of them."""
+    gemm = dict(x_q=on(0, 64, 64), x_s=on(0, 64, 2), w_q=on(0, 2, 32, 64), w_s=on(0, 2, 32, 2),
+                offsets=on(0, 3, dtype=torch.int32), out=on(0, 64, 32, dtype=torch.bfloat16))
+    wgrad = dict(g_q=on(0, 32, 64), g_s=on(0, 32, 2), x_q=on(0, 64, 64), x_s=on(0, 64, 2),
+                 offsets=on(0, 3, dtype=torch.int32), out=on(0, 2, 32, 64, dtype=torch.float32))
+    gemv = dict(x=on(0, 2, 64, dtype=torch.bfloat16), w_q=on(0, 3, 32, 32), w_s=on(0, 3, 32, 4),
+                global_scale=on(0, 3, dtype=torch.float32), experts=on(0, 2, dtype=torch.int32),
+                out=on(0, 2, 32, dtype=torch.bfloat16))
+    return [(mxq.mx_grouped_gemm, gemm), (mxq.mx_grouped_wgrad, wgrad), (mxq.nvfp4_gemv, gemv)]
+
+
+def test_bindings_refuse_what_lies_elsewhere(monkeypatch):
+    """Operands, outputs and the error word on another device than the first
+    operand's, a first operand not on the current device, host memory: none of
+    them reaches the library."""
+    class Reached(Exception):
+        pass
+
+    class Library:
+        def __getattr__(self, name):
+            def entry(*args):
+                raise Reached
+            return entry
+
+    monkeypatch.setattr(mxq._lib, "lib", Library)
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(mxq, "_several", None, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0)
+    for call, args in product_calls():
+        with pytest.raises(Reached):
+            call(**args)
+        err = on(0, 1, dtype=torch.int32)
+        with pytest.raises(Reached):
+            call(**args, dev_err=err)
+        for name, t in args.items():
+            for at, error in ((1, ValueError), (-1, (TypeError, ValueError))):
+                other = t.clone().as_subclass(OnDevice)
+                other.at = at
+                with pytest.raises(error):
+                    call(**{**args, name: other})
+            with pytest.raises(TypeError):
+                call(**{**args, name: t.tolist()})
+        with pytest.raises(ValueError):
+            call(**args, dev_err=on(1, 1, dtype=torch.int32))
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+        with pytest.raises(ValueError):
+            call(**args)
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+        # Without another device there is nothing to compare.
+        monkeypatch.setattr(mxq, "_several", False)
+        for bad in (torch.zeros(1, dtype=torch.int32), on(0, 0, dtype=torch.int32), on(0, 4), [0], 0):
+            with pytest.raises(TypeError):
+                call(**args, dev_err=bad)
+        with pytest.raises((TypeError, ValueError)):
+            call(**{**args, "out": args["out"].as_subclass(torch.Tensor)})
+        monkeypatch.setattr(mxq, "_several", None)
+
+
 @gpu
 @pytest.mark.parametrize("exact", [True, False], ids=["exact", "random"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
