@@ -489,8 +489,9 @@ mx_grouped_kernel(const __grid_constant__ GroupedMaps maps, const GroupedArgs a)
   } else if (warp >= 4) {
     // ---- scales: thread t takes piece t % 4 of rows t / 4 + 32 i of this
     // CTA's A rows and of all of B's, so that a row's 64 bytes are one request,
-    // and a thread's rows one 16-byte unit of each stage's tile.  The loads run
-    // a chunk before the stores, over the ends of tiles too. ----
+    // and a thread's rows one 16-byte unit of each stage's tile.  A window's loads
+    // are all in flight at once, and then its stores wait for places; a second
+    // window does not fit the registers. ----
     const int piece = tid % 4, r = (tid - 128) / 4;
     const int64_t a_total = KIND == FORWARD ? a.limit
                             : KIND == FEW   ? static_cast<int64_t>(a.groups) * a.a_rows : a.a_rows;

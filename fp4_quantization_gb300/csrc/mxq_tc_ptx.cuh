@@ -235,16 +235,8 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src,
       :: "l"(map), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
 }
 
-// 2-D TMA tile load into this CTA's shared memory, completing on a barrier of
+// 3-D TMA tile load into this CTA's shared memory, completing on a barrier of
 // the pair's first CTA (an address of cluster_addr).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x,
-                                                 int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];"
-      :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
-}
-
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x,
                                                  int y, int z, uint32_t bar) {
   asm volatile(
