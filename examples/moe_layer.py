@@ -6,11 +6,12 @@ in MXFP8 and one decoding step with NVFP4 weights.
 Training (all operands quantized by the library, every product one of its
 grouped products):
 
-    x -> MXFP8 -> [gate | up] = x W1^T -> SwiGLU -> MXFP8 -> y = h W2^T
-    dy -> MXFP8 -> dh = dy W2 -> dSwiGLU -> MXFP8 -> dx = d[gate | up] W1
-    dW2 = dy^T h,  dW1 = d[gate | up]^T x
+    x -> MXFP8 -> [gate | up] = x W1^T -> SwiGLU -> MXFP8 -> f = h W2^T
+    df -> MXFP8 -> dh = df W2 -> dSwiGLU -> MXFP8 -> dx = d[gate | up] W1
+    dW2 = df^T h,  dW1 = d[gate | up]^T x
 
-Rows are sorted by expert, each expert's padded with zero rows to a multiple of
+A token's experts are summed by its router's weights: y = sum_j p_j f_j, so that
+df_j = p_j dy and dp_j = dy . f_j.  Without weights every p_j is one.  Rows are sorted by expert, each expert's padded with zero rows to a multiple of
 32, so that no block of 32 rows belongs to two experts.  Decoding multiplies the
 few rows of a step with the experts' 4-bit weights where they lie.
 """
@@ -52,20 +53,23 @@ class MXWeights:
             torch.stack([d[k] for d in q]) for k in ("q_row", "s_row", "q_col", "s_col"))
 
 
-def train_step(x, experts, w1, w2, dy):
+def train_step(x, experts, w1, w2, dy, weights=None):
     """x [T, H] bf16, experts [T, k], w1 [E, 2F, H] and w2 [E, H, F] as MXWeights,
     dy [T, H]: y and dx [T, H] (summed over a token's experts) and the
-    weights' gradients in fp32."""
+    weights' gradients in fp32; with the router's weights [T, k] fp32, their
+    gradient too."""
     T, k = experts.shape
     row, offsets, rows = sort_rows(experts, w1.q.shape[0])
 
-    def scatter(t):
+    def scatter(t, weights=None):
         out = torch.zeros(rows, t.shape[1], dtype=torch.bfloat16, device=t.device)
-        out[row] = t.repeat_interleave(k, 0)
+        t = t.repeat_interleave(k, 0)
+        out[row] = t if weights is None else (t * weights.view(-1, 1)).bfloat16()
         return out
 
-    def gather(t):
-        return t[row].view(T, k, -1).float().sum(1).bfloat16()
+    def gather(t, weights=None):
+        t = t[row].view(T, k, -1).float()
+        return (t if weights is None else t * weights.unsqueeze(-1)).sum(1).bfloat16()
 
     def rows_product(q, w, w_s):
         # The padding after the last group belongs to no expert and stays zero.
@@ -75,15 +79,18 @@ def train_step(x, experts, w1, w2, dy):
     xq = mxq.mx_quantize_rowcol(scatter(x))
     gate_up = rows_product(xq, w1.q, w1.s)
     hq = mxq.mx_quantize_gated(gate_up)
-    y = rows_product(hq, w2.q, w2.s)
+    f = rows_product(hq, w2.q, w2.s)
 
-    gq = mxq.mx_quantize_rowcol(scatter(dy))
+    gq = mxq.mx_quantize_rowcol(scatter(dy, weights))
     dh = rows_product(gq, w2.q_t, w2.s_t)
     dgq = mxq.mx_quantize_dgated(dh, gate_up)
     dx = rows_product(dgq, w1.q_t, w1.s_t)
     dw1 = mxq.mx_grouped_wgrad(dgq["q_col"], dgq["s_col"], xq["q_col"], xq["s_col"], offsets)
     dw2 = mxq.mx_grouped_wgrad(gq["q_col"], gq["s_col"], hq["q_col"], hq["s_col"], offsets)
-    return gather(y), gather(dx), dw1, dw2
+    if weights is None:
+        return gather(f), gather(dx), dw1, dw2
+    dweights = (f[row].view(T, k, -1).float() * dy.float().unsqueeze(1)).sum(-1)
+    return gather(f, weights), gather(dx), dw1, dw2, dweights
 
 
 class NVWeights:
@@ -96,16 +103,16 @@ class NVWeights:
         self.g = self.g.flatten()
 
 
-def decode_step(x, experts, w1, w2):
+def decode_step(x, experts, w1, w2, weights=None):
     """x [T, H] bf16, experts [T, k], w1 [E, 2F, H] and w2 [E, H, F] as
-    NVWeights: y [T, H]."""
+    NVWeights, the router's weights [T, k] fp32 or none: y [T, H]."""
     T, k = experts.shape
     ids = experts.flatten().int()
     gate_up = mxq.nvfp4_gemv(x, w1.q, w1.s, w1.g, experts=ids, share=k, out_dtype=torch.float32)
     gate, up = gate_up.chunk(2, 1)
     h = (torch.nn.functional.silu(gate) * up).bfloat16()
-    y = mxq.nvfp4_gemv(h, w2.q, w2.s, w2.g, experts=ids, out_dtype=torch.float32)
-    return y.view(T, k, -1).sum(1).bfloat16()
+    f = mxq.nvfp4_gemv(h, w2.q, w2.s, w2.g, experts=ids, out_dtype=torch.float32).view(T, k, -1)
+    return (f if weights is None else f * weights.unsqueeze(-1)).sum(1).bfloat16()
 
 
 def main():
@@ -117,11 +124,12 @@ def main():
 
     w1, w2 = draw(E, 2 * F, H, scale=H ** -0.5), draw(E, H, F, scale=F ** -0.5)
     x, dy = draw(T, H), draw(T, H)
-    experts = torch.rand(T, E, generator=gen, device="cuda").topk(k, 1).indices
-    y, dx, dw1, dw2 = train_step(x, experts, MXWeights(w1), MXWeights(w2), dy)
+    scores, experts = (x.float() @ draw(E, H, scale=H ** -0.5).float().t()).topk(k, 1)
+    p = scores.softmax(1)
+    y, dx, dw1, dw2, dp = train_step(x, experts, MXWeights(w1), MXWeights(w2), dy, p)
     print("training:", *(f"{n} {tuple(t.shape)} norm {t.float().norm():.4g}"
-                         for n, t in (("y", y), ("dx", dx), ("dw1", dw1), ("dw2", dw2))))
-    z = decode_step(x[:4], experts[:4], NVWeights(w1), NVWeights(w2))
+                         for n, t in (("y", y), ("dx", dx), ("dw1", dw1), ("dw2", dw2), ("dp", dp))))
+    z = decode_step(x[:4], experts[:4], NVWeights(w1), NVWeights(w2), p[:4])
     off = (z.float() - y[:4].float()).norm() / y[:4].float().norm()
     print(f"decoding: y {tuple(z.shape)}, {off:.3f} from the MXFP8 rows")
 

@@ -67,3 +67,45 @@ def test_decoding_step(T, k, E, H, F):
     got = moe_layer.decode_step(x, experts, moe_layer.NVWeights(w1), moe_layer.NVWeights(w2))
     want = layer(x.float(), experts, w1.float(), w2.float())
     assert off(got, want) <= 2 * NVFP4
+
+
+def weighted_layer(x, experts, w1, w2, weights):
+    """The layer in fp32 with a router's weights, differentiable."""
+    y = torch.zeros_like(x)
+    for e in range(len(w1)):
+        token, slot = (experts == e).nonzero(as_tuple=True)
+        gate, up = (x[token] @ w1[e].t()).chunk(2, 1)
+        f = (torch.nn.functional.silu(gate) * up) @ w2[e].t()
+        y = y.index_add(0, token, f * weights[token, slot].unsqueeze(1))
+    return y
+
+
+def draw_weights(experts, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed + 1)
+    return torch.randn(experts.shape, generator=gen, device="cuda").softmax(1)
+
+
+@pytest.mark.parametrize("T,k,E,H,F", [(200, 2, 6, 256, 384), (64, 4, 4, 160, 64)])
+def test_training_step_with_router_weights(T, k, E, H, F):
+    import moe_layer
+
+    x, experts, w1, w2, dy = draw(T, k, E, H, F, T)
+    weights = draw_weights(experts, T)
+    got = moe_layer.train_step(x, experts, moe_layer.MXWeights(w1), moe_layer.MXWeights(w2), dy, weights)
+    leaves = [t.float().requires_grad_() for t in (x, w1, w2, weights)]
+    want_y = weighted_layer(leaves[0], experts, *leaves[1:])
+    want = (want_y, *torch.autograd.grad(want_y, leaves, dy.float()))
+    # As test_training_step; the weights' gradients are dy times what y sums.
+    for t, exact, steps in zip(got, want, (4, 6, 6, 4, 4)):
+        assert off(t, exact.detach()) <= steps * E4M3
+
+
+@pytest.mark.parametrize("T,k,E,H,F", [(1, 2, 8, 256, 384), (5, 3, 16, 512, 160)])
+def test_decoding_step_with_router_weights(T, k, E, H, F):
+    import moe_layer
+
+    x, experts, w1, w2, _ = draw(T, k, E, H, F, T)
+    weights = draw_weights(experts, T)
+    got = moe_layer.decode_step(x, experts, moe_layer.NVWeights(w1), moe_layer.NVWeights(w2), weights)
+    want = weighted_layer(x.float(), experts, w1.float(), w2.float(), weights)
+    assert off(got, want) <= 2 * NVFP4
