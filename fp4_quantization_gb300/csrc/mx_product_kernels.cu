@@ -7,8 +7,9 @@
 // in fp32 in tensor memory.
 //
 // Large calls are bound by the board's power and then by the tensor pipe (8192
-// rows over 8 experts, 4096 x 8192: 186 us, 3.0 PFLOP/s, and 166 on zero codes, at
-// which the clock stays up; 16384 rows, 14336 x 4096: 647 and 546 us), calls with
+// rows over 8 experts, 4096 x 8192: 187 us, 2.9 PFLOP/s, for the first hundred
+// calls, 191-205 on and on, 166 on zero codes, at which the clock stays up; 16384
+// rows, 14336 x 4096: 632-647, 672-705 and 546 us), calls with
 // few rows an expert by reading the weights (36 rows over 41 experts, 5866 x
 // 1344: 33 us, 5.9 TB/s), weight gradients of short groups by writing them (64
 // experts x 1408 x 2048 fp32: 132 us, 5.8 TB/s).
