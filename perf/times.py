@@ -7,7 +7,7 @@ a CUDA graph of twelve; `call`, microseconds a call from Python, one after anoth
 both by CUDA events, the least of five runs after a warm-up.  `floor` is the larger
 of the case's bytes and its operations at this GPU's measured rates (with the MXFP8
 instruction at twice the bf16 rate).  Where power bounds a call the clock drops, so
-that the figures of large calls move by some percent between boxes.
+that the figures of large calls move by some percent between machines.
 """
 import argparse
 import json
