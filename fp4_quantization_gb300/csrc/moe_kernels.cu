@@ -754,6 +754,16 @@ struct SortShared {
   __host__ __device__ static constexpr int bytes(int experts) { return 4 * words(experts) + 8 * PAIRS; }
 };
 
+// The cluster's barrier in two halves, for lanes that come apart: E experts and the rows
+// past the last expert's end inside a warp, so that neither is the aligned form, which
+// wants a whole warp at once.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 template <int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) moe_sort_kernel(const SortArgs a) {
   constexpr int THREADS = 32 * WARPS;
@@ -829,7 +839,8 @@ __global__ void __launch_bounds__(32 * WARPS) moe_sort_kernel(const SortArgs a) 
     }
     total[tid] = own;
   }
-  cluster.sync();
+  cluster_arrive();
+  cluster_wait();
   // Over the CTAs, and over the experts: first rows of padded groups, and first places.
   int32_t before = 0, size = 0;
   if (tid < E) {
@@ -841,7 +852,7 @@ __global__ void __launch_bounds__(32 * WARPS) moe_sort_kernel(const SortArgs a) 
     }
   }
   // The other CTAs' totals have been read: they may leave once all have come here.
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  cluster_arrive();
   const int32_t padded = (size + a.align - 1) / a.align * a.align;
   int32_t x = own, y = padded;
 #pragma unroll
@@ -914,7 +925,7 @@ __global__ void __launch_bounds__(32 * WARPS) moe_sort_kernel(const SortArgs a) 
          r += static_cast<int64_t>(ctas) * THREADS)
       a.source[r] = -1;
   }
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_wait();
 }
 
 template <int WARPS>

@@ -337,6 +337,22 @@ def test_sort(n, E, align):
         bufs[name][1]()
 
 
+# Clusters of 1, 2, 4, 8 and 16 CTAs, and pairs in registers or not; experts and rows of
+# no pair that end inside a warp, so that its lanes reach the cluster's barriers apart.
+@gpu
+@pytest.mark.parametrize("n", [600, 1024, 2048, 4096, 8192, 16000, 262145])
+@pytest.mark.parametrize("E", [1, 17, 33, 257, 511])
+def test_sort_with_lanes_apart(n, E):
+    gen = torch.Generator(device="cuda").manual_seed(n + E)
+    e = torch.randint(0, E, (n,), generator=gen, device="cuda").int()
+    first = mxq.moe_sort(e, E, align=7)
+    for name, want in sort_reference(e, E, 7, mxq.moe_sort_rows(n, E, 7)).items():
+        assert first[name].tolist() == want, name
+    for _ in range(20):
+        again = mxq.moe_sort(e, E, align=7)
+        assert all(torch.equal(again[name], first[name]) for name in first)
+
+
 @gpu
 def test_sort_shapes():
     e = torch.randint(0, 16, (100, 4), device="cuda").int()
