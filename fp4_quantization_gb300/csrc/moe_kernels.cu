@@ -504,6 +504,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, ROUTE_CTAS) moe_route_kernel
     sk = s_keys[warp];          // the logits stay as they are
     __syncwarp();
     store_values(sk + e0, key);
+    __syncwarp();               // expert() reads other lanes' keys
   }
   sort_descending(key);
   if (grouped && ch.own >= 0) {

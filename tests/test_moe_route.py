@@ -108,6 +108,21 @@ def test_groups(T, E, groups, kept, k, flags, gmax):
 
 @gpu
 @pytest.mark.parametrize("flags", MODES)
+@pytest.mark.parametrize("E,groups,kept", [(36, 3, 2), (120, 8, 4), (160, 5, 2), (500, 20, 7)])
+def test_groups_that_lanes_share(E, groups, kept, flags):
+    """Groups that begin or end inside a lane's experts: a chosen key's expert is looked
+    up among keys that another lane has masked.  Many tokens, many times."""
+    l, gen = draw(6000, E, E)
+    bias = torch.randn(E, generator=gen, device="cuda") * 0.1
+    for kw in ({}, {"bias": bias}):
+        first = check_route(l, 6, flags, groups=groups, kept=kept, **kw)
+        for _ in range(10):
+            again = mxq.moe_route(l, 6, flags, groups=groups, kept=kept, **kw)
+            assert all(torch.equal(a, b) for a, b in zip(again, first))
+
+
+@gpu
+@pytest.mark.parametrize("flags", MODES)
 def test_masked_experts(flags):
     l, gen = draw(400, 48, 3)
     l[torch.rand(400, 48, generator=gen, device="cuda") < torch.linspace(0, 1, 400, device="cuda")[:, None]] = -math.inf
