@@ -171,7 +171,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// (The aligned forms want the whole warp at once: lanes that came apart join first.)
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                ::: "memory");
 }
