@@ -581,7 +581,20 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, ROUTE_CTAS) moe_route_kernel
       // The same logit and bias are a true tie, in the order of the experts.
       const float x = chosen >= 0 ? sl[chosen] : none, b = chosen >= 0 ? a.bias[chosen] : 0.0f;
       const float x2 = __shfl_down_sync(FULL, x, 1), b2 = __shfl_down_sync(FULL, b, 1);
-      if (__any_sync(FULL, near && (lane == 31 || x != x2 || b != b2))) {
+      bool differ = near && (lane == 31 || x != x2 || b != b2);
+      // A tie of the last slot and the next key may hide others that are as near behind
+      // it: any expert within the limit that is not tied with them.
+      if (!__any_sync(FULL, differ) && __shfl_sync(FULL, near, a.slots - 1)) {
+        const float last = __shfl_sync(FULL, slot_key, a.slots - 1);
+        const float xl = __shfl_sync(FULL, x, a.slots - 1), bl = __shfl_sync(FULL, b, a.slots - 1);
+#pragma unroll 1
+        for (int e = lane; e < a.experts; e += 32) {
+          const float k = sk[e];
+          if (k > none && last - k <= 2.0f * err + 1.2e-7f * (fabsf(last) + fabsf(k)))
+            differ = differ || sl[e] != xl || a.bias[e] != bl;
+        }
+      }
+      if (__any_sync(FULL, differ)) {
         const float last = __shfl_sync(FULL, slot_key, a.slots - 1);
         const float border = last - 2.0f * (2.0f * err + 2.4e-7f * fabsf(last));
         // Every expert that may be among the chosen, a lane each.

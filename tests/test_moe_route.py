@@ -179,6 +179,53 @@ def test_ties_and_near_ties(flags):
                 bias=torch.zeros(E, device="cuda"))
 
 
+# The fp32 keys of a last slot and the next expert tie by the same logit and bias, and a
+# third one stands within their error behind them.
+@gpu
+@pytest.mark.parametrize("flags,k,logits,bias,want", [
+    (SIG, 1, (20, 20, 20.5), (0, 0, 0), [2]),
+    (SIG, 1, (17.5, 17.5, 18), (0, 0, 0), [2]),
+    (SIG, 2, (25, 17.5, 17.5, 18, 17.5), (0, 0, 0, 0, 0), [0, 3]),
+    (SIG, 1, (17.5, 17.5, 17.5, 3), (0, 0, 0, 0.03), [0]),
+    (0, 1, (0, 0, 1e-8), (0, 0, 0), [2]),
+    (0, 2, (10, -8, -8, -7.96875), (0, 0.25, 0.25, 0.25), [0, 3]),
+    (0, 2, (10, -8, -8, -8.03125), (0, 0.25, 0.25, 0.25), [0, 1]),
+])
+def test_near_behind_a_tie(flags, k, logits, bias, want):
+    bias = torch.tensor(bias, dtype=torch.float32, device="cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        if dtype == torch.bfloat16 and 1e-8 in logits:
+            continue
+        l = torch.tensor([logits] * 5, dtype=dtype, device="cuda")
+        for renorm in (0, RENORM):
+            e, _ = check_route(l, k, flags | renorm, bias=bias)
+            assert e.tolist() == [want] * 5
+
+
+@gpu
+@pytest.mark.parametrize("flags", MODES)
+@pytest.mark.parametrize("E,groups,kept", [(24, 1, 1), (64, 1, 1), (256, 1, 1), (500, 1, 1), (64, 8, 5), (256, 8, 6), (120, 8, 6), (384, 6, 5)])
+@pytest.mark.parametrize("k", [1, 2, 5, 8, 31, 32])
+def test_near_behind_many_ties(E, groups, kept, k, flags):
+    """Experts of the same logit and bias, and some that are better by less than fp32
+    shows, few or many, among them anywhere."""
+    T = 300
+    gen = torch.Generator(device="cuda").manual_seed(E + k)
+    if k > E // groups * kept:
+        k = E // groups * kept
+    rate = torch.tensor([0.0, 1 / E, 4 / E, 0.2, 0.9], device="cuda")[torch.arange(T, device="cuda") % 5, None]
+    better = torch.rand(T, E, generator=gen, device="cuda") < rate
+    if flags & SIG:
+        l = torch.where(better, 18.0, 17.5)
+    else:
+        l = torch.where(better, 1e-8, 0.0)
+    step = torch.where(torch.rand(E, generator=gen, device="cuda") < 0.5, 0.0, 0.125)
+    for bias in (torch.zeros(E, device="cuda"), torch.full((E,), -0.375, device="cuda"), step):
+        check_route(l, k, flags, bias=bias, groups=groups, kept=kept)
+        if flags & SIG:
+            check_route(l.bfloat16(), k, flags, bias=bias, groups=groups, kept=kept)
+
+
 @gpu
 def test_many_tokens_and_large_logits():
     l, gen = draw(20000, 64, 8, spread=30.0)
