@@ -609,7 +609,9 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, ROUTE_CTAS) moe_route_kernel
           // those behind it by that is seen without 64 bits (8192 tokens, 8 of 256 with a
           // bias: 13.6 us, 14.6 without).
           const float l0 = chosen >= 0 ? sl[chosen] : none;
-          const float off = (sigmoid ? err : score(l0) * (3.0e-6f + 1.6e-7f * (top - l0)) + 2e-38f) +
+          // (From 88 on a score is 0 here, and the difference may be infinite.)
+          const float apart = fminf(top - l0, 1000.0f);
+          const float off = (sigmoid ? err : score(l0) * (3.0e-6f + 1.6e-7f * apart) + 2e-38f) +
                             2.4e-7f * fabsf(slot_key);
           float behind = __shfl_down_sync(FULL, chosen >= 0 ? slot_key + off : none, 1);
           if (lane == 31) behind = none;

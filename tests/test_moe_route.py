@@ -227,6 +227,23 @@ def test_near_behind_many_ties(E, groups, kept, k, flags):
 
 
 @gpu
+@pytest.mark.parametrize("renorm", [0, RENORM])
+def test_logits_apart_by_more_than_fp32(renorm):
+    """Softmax logits whose differences are infinite in fp32: a score of zero, whose key is
+    its bias exactly, beside thirds that their rounding alone tells from it."""
+    third = torch.tensor(1 / 3, dtype=torch.float32)
+    below = torch.nextafter(third, torch.zeros(()))
+    above = torch.nextafter(third, torch.ones(()))
+    for b in (third, below, above):
+        for order in ([0, 1, 2, 3], [3, 0, 1, 2], [1, 3, 0, 2]):
+            l = torch.tensor([2e38, 2e38, 2e38, -2e38], device="cuda")[order].repeat(3, 1)
+            bias = torch.tensor([0, -1, -1, float(b)], device="cuda")[order]
+            for k in (1, 2, 3):
+                check_route(l, k, renorm, bias=bias)
+                check_route(l.bfloat16(), k, renorm, bias=bias)
+
+
+@gpu
 def test_many_tokens_and_large_logits():
     l, gen = draw(20000, 64, 8, spread=30.0)
     for flags in MODES:
