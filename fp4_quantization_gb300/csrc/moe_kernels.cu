@@ -455,7 +455,8 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, ROUTE_CTAS) moe_route_kernel
     const int g = lane >> spread;
     const bool in = g < a.groups;
     const bool alone = (a.flags & MXQ_ROUTE_GROUP_MAX) || ch.group_size == 1;
-    const float s = alone ? t1 : t1 + t2;
+    // (The mean of the two: their sum may pass fp32's range.)
+    const float s = 0.5f * t1 + 0.5f * (alone ? t1 : t2);
     // The best group a.kept times, and the next one's score; equal groups in order.
     uint32_t keep = 0u;
     float rest = in ? s : none, worst = none;
@@ -467,10 +468,10 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, ROUTE_CTAS) moe_route_kernel
       left = left && g != first >> spread;
     }
     const float next = redux_max(left ? rest : none);
-    // Two scores a side, each off by err and, with its bias, a rounding, and the
+    // The mean of two scores a side, each off by err and, with its bias, a rounding, and the
     // rounding of their sum.  Groups at -inf are behind the others, and a tie.
     const float amp = redux_max((t1 > none ? fabsf(t1) : 0.0f) + (t2 > none ? fabsf(t2) : 0.0f));
-    if (!(next > none && worst - next <= 4.0f * err + 2.4e-7f * amp)) return keep;
+    if (!(next > none && worst - next <= 2.0f * err + 1.2e-7f * amp)) return keep;
     // Every expert that may be one of its group's two best, a lane each: logits have
     // their own order, keys are off by err and a rounding.
     const float slack = a.bias ? 2.0f * err + 2.4e-7f * (fabsf(second) + 1.0f) : 0.0f;

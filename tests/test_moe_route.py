@@ -244,6 +244,20 @@ def test_logits_apart_by_more_than_fp32(renorm):
 
 
 @gpu
+@pytest.mark.parametrize("flags", [0, SIG])
+def test_groups_of_huge_biases(flags):
+    """Sums of two keys that pass fp32's range, upwards and downwards."""
+    l, _ = draw(9, 16, 3)
+    for values in ([1e38, 3e38, 2e38, -3e38], [-3e38, -2e38, -3.2e38, -2.5e38], [3e38, 3e38, 3.1e38, 1.0]):
+        bias = torch.tensor(values, device="cuda").repeat_interleave(4)
+        for kept in (1, 2, 3):
+            for gmax in (0, GMAX):
+                check_route(l, 4, flags | gmax, bias=bias, groups=4, kept=kept)
+        # Groups that a lane's experts do not fill.
+        check_route(l[:, :12].contiguous(), 3, flags, bias=bias[:12].contiguous(), groups=3, kept=1)
+
+
+@gpu
 def test_many_tokens_and_large_logits():
     l, gen = draw(20000, 64, 8, spread=30.0)
     for flags in MODES:
