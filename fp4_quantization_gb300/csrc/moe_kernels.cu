@@ -11,6 +11,7 @@
 // scores.  That happens to about one token in a thousand.
 
 #include <cooperative_groups.h>
+#include <cfloat>
 
 #include "mxq_internal.h"
 #include "mxq_layer.h"
@@ -710,17 +711,18 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) moe_route_back_kernel(const 
     const float s = real ? expf(li - top) * inv : 0.0f;
     d = g * s;
     share = warp_add(d);
-    for (int x = lane; x < a.experts; x += 32) sg[x] = -(sg[x] * inv) * share;
+    // A token without an expert has no gradient, whatever its logits.
+    for (int x = lane; x < a.experts; x += 32) sg[x] = share == 0.0f ? 0.0f : -(sg[x] * inv) * share;
   } else {
     for (int x = lane; x < a.experts; x += 32) sg[x] = 0.0f;
     if (!renorm) {
       d = real ? g * sigmoid_of(li) * sigmoid_of(-li) : 0.0f;
     } else {
       const float low = !real ? -infinity() : sigmoid ? fminf(li, 0.0f) : li;
-      const float most = warp_max(low);
+      const float most = fmaxf(warp_max(low), -FLT_MAX);     // chosen scores may all be 0
       float x = real ? expf(low - most) : 0.0f;
       if (sigmoid && real) x *= sigmoid_n(li);
-      const float sum = warp_add(x);
+      const float sum = fmaxf(warp_add(x), 0.25f);           // 1 / 2 at least where one is not
       const float w = real ? x / sum : 0.0f;
       const float c = warp_add(g * w);
       d = w * (g - c);

@@ -369,6 +369,60 @@ def test_backward_odd_choices(flags):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("flags", MODES)
+def test_backward_where_no_gradient_reaches(flags, dtype):
+    """Tokens without an expert, whatever their logits, and slots whose experts' scores
+    are all zero: the gradient is zero there, and other tokens' are as without them."""
+    l, gen = draw(12, 40, 6, dtype)
+    e, _ = mxq.moe_route(l, 4, flags)
+    dw = torch.randn(12, 4, generator=gen, device="cuda")
+    want = mxq.moe_route_backward(dw, l, e, flags)
+    bad = l.clone()
+    bad[1, 7] = math.nan
+    bad[2, 3] = math.inf
+    bad[3] = math.nan
+    bad[4] = -math.inf
+    bad[5, 20:] = -math.inf
+    chosen, w = mxq.moe_route(bad, 4, flags)
+    chosen[5] = torch.tensor([20, 21, 39, -1])
+    got = mxq.moe_route_backward(dw, bad, chosen, flags)
+    assert (chosen[1:5] == -1).all() and not got[1:6].any()
+    keep = [0, *range(6, 12)]
+    assert torch.equal(got[keep], want[keep])
+
+
+@gpu
+@pytest.mark.parametrize("spread", [1.0, 6.0, 25.0])
+@pytest.mark.parametrize("flags", MODES)
+def test_backward_of_small_scores(flags, spread):
+    """Gradients in proportion to their own scores, however small those are.  A weight or
+    score is off by 100 2^-24 of itself (spreads of 30 and more: by |l - top| 2^-24 besides),
+    g - c by that of |g| + |c|, and a chosen score's own part and the row's are added."""
+    l, gen = draw(300, 64, 11, spread=spread)
+    e, _ = mxq.moe_route(l, 6, flags)
+    dw = torch.randn(300, 6, generator=gen, device="cuda")
+    got = mxq.moe_route_backward(dw, l, e, flags, scale=2.0).double()
+    # By the formulas: differences of scores near one would leave rounding in 64 bits too.
+    l64, g, at = l.double(), 2 * dw.double(), e.long()
+    s = scores64(l64, bool(flags & SIG))
+    if flags & RENORM:
+        chosen = l64.gather(1, at)
+        w = (torch.nn.functional.logsigmoid(chosen) if flags & SIG else chosen).softmax(1)
+        slope = scores64(-chosen, True) if flags & SIG else torch.ones_like(w)
+        want = torch.zeros_like(s).scatter_(1, at, w * (g - (g * w).sum(1, keepdim=True)) * slope)
+        s = torch.zeros_like(s).scatter_(1, at, w * slope)
+    elif flags & SIG:
+        s = s * scores64(-l64, True)
+        want = torch.zeros_like(s).scatter_(1, at, g) * s
+    else:
+        want = s * (torch.zeros_like(s).scatter_(1, at, g) - (g * s.gather(1, at)).sum(1, keepdim=True))
+    steps = 100 + (l.amax(1, keepdim=True) - l.amin(1, keepdim=True)).double()
+    bound = 2 * steps * U * s * (2.0 * 2 * dw.abs().amax(1, keepdim=True).double()) + 1e-37
+    assert ((got - want).abs() <= bound).all()
+
+
+@gpu
 @pytest.mark.parametrize("flags", MODES)
 def test_backward_against_differences(flags):
     l, gen = draw(3, 10, 4)
