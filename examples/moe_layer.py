@@ -29,7 +29,9 @@ import fp4_quantization_gb300 as mxq  # noqa: E402
 def sort_rows(experts, num_experts):
     """Where each (token, expert) pair goes: its row in the buffer sorted by
     expert, the group offsets [E + 1] (multiples of 32), and the buffer's rows
-    (a bound that needs no copy to the host)."""
+    (a bound that needs no copy to the host).  A pair without an expert has row -1,
+    which indexes the last one: with such a pair the bound is longer than the groups,
+    and that row is no expert's."""
     out = mxq.moe_sort(experts.int().contiguous(), num_experts, align=32)
     return out["rows"].flatten().long(), out["offsets"], len(out["source"])
 
@@ -45,8 +47,8 @@ class MXWeights:
 
 
 def train_step(x, experts, w1, w2, dy, weights=None, checkpoint=False):
-    """x [T, H] bf16, experts [T, k], w1 [E, 2F, H] and w2 [E, H, F] as MXWeights,
-    dy [T, H]: y and dx [T, H] (summed over a token's experts) and the
+    """x [T, H] bf16, experts [T, k] (-1: none), w1 [E, 2F, H] and w2 [E, H, F]
+    as MXWeights, dy [T, H]: y and dx [T, H] (summed over a token's experts) and the
     weights' gradients in fp32; with the router's weights [T, k] fp32, their
     gradient too.  With `checkpoint` the backward pass reads [gate | up], the
     largest activation, in 8 bits, so that its bf16 form need not be kept."""

@@ -89,6 +89,31 @@ def test_checkpoint_in_the_layer():
         assert 0 < off(t, s.float()) <= 2 * E4M3
 
 
+@pytest.mark.parametrize("checkpoint", [False, True])
+@pytest.mark.parametrize("T,E", [(1, 3), (40, 4), (96, 2)])
+def test_slots_without_an_expert(T, E, checkpoint):
+    """They add nothing, wherever they stand: not to the outputs, and not to the rows
+    that pad another expert's (one pair of one expert fills 32 of them)."""
+    import moe_layer
+
+    x, _, _, _, w1, w2, dy = draw(T, E, 128, 96, T)
+    w1, w2 = moe_layer.MXWeights(w1), moe_layer.MXWeights(w2)
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    experts = torch.randint(0, E, (T, 1), generator=gen, device="cuda")
+    p = torch.rand(T, 1, generator=gen, device="cuda")
+    for weights in (None, p):
+        want = moe_layer.train_step(x, experts, w1, w2, dy, weights, checkpoint)
+        none = torch.full_like(experts, -1)
+        more = None if weights is None else torch.cat((0 * p, p, 1 + p), 1)
+        got = moe_layer.train_step(x, torch.cat((none, experts, none), 1), w1, w2, dy, more, checkpoint)
+        if weights is not None:
+            assert not got[4][:, 0].any() and not got[4][:, 2].any()
+            assert torch.equal(got[4][:, 1:2], want[4])
+        # (Sums of the same terms, which buffers of another length may cut otherwise.)
+        for s, t in zip(got[:4], want[:4]):
+            assert (s.double() - t.double()).norm() <= 2.0 ** -7 * t.double().norm()
+
+
 # ---------------------------------------------------------------------------
 # Streams, graphs, calls side by side
 # ---------------------------------------------------------------------------
