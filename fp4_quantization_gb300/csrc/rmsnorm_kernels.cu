@@ -636,14 +636,17 @@ cudaError_t launch_norm_rows(const NormArgs& a, int num_sms, cudaStream_t stream
   // with two 3.1, with three 3.6), and in narrow ones.  Else two, in as many warps as the
   // row fills: 16384 x 5120 without a residual takes 47 us in five warps, 59 in eight; with
   // a residual 87 and 92.  Long runs without a residual, whose loads are half as many, have
-  // three (9824 x 10240 59 us, with two 64), or four where they are as many as lanes
-  // (12288 x 8192 57 us, with two 60, with three 58), and narrow ones two (16384 x 1024
-  // 10.6 us, with one 11.3; rstd alone 14.7 and 18.2 with the columns).
+  // three (9824 x 10240 59 us, with two 64), and narrow ones two (16384 x 1024 10.6 us, with
+  // one 11.3; rstd alone 14.7 and 18.2 with the columns).  They have four where that is
+  // four or eight warps with fewer idle lanes than three granules leave, above 7680 and
+  // 15360 columns (rows of 134 M values, us with four and with three: 7424 columns 77.0, 72.6;
+  // 7712 77.1, 80.1; 8192 72.9, 75.6; 10240, in five warps, 81.7, 77.0; 14336, in seven,
+  // 81.7, 77.7; 15360 80.2, 75.8; 15392 81.9, 96.6; 16384 77.4, 91.0).
   const bool few = a.M <= 2 * num_sms, deep = !a.residual && a.M >= 32 * num_sms;
   if (deep && granules > 320 && granules <= 1024) {
-    if (granules == 512) return launch_rows<4, 4>(a, stream);
-    if (granules == 1024) return launch_rows<8, 4>(a, stream);
-    return launch_rows_of<3, 4, 5, 6, 7, 8, 9, 10, 11>(a, stream);
+    const int three = (granules + 95) / 96, four = (granules + 127) / 128;     // warps
+    if (four % 4 == 0 && 128 * four < 96 * three) return launch_rows_of<4, 4, 8>(a, stream);
+    return launch_rows_of<3, 4, 5, 6, 7, 8, 9, 10>(a, stream);
   }
   if (granules <= 32 || (granules <= 128 && !deep) || (granules <= 1024 && few))
     return launch_rows_of<1, 1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32>(a, stream);

@@ -185,6 +185,12 @@ def test_rows_alone_and_among_many(K):
     assert torch.equal(alone["rstd"], many["rstd"][:4992])
 
 
+@gpu
+@pytest.mark.parametrize("K", [7648, 7680, 7712, 8160, 8224, 15360, 15392, 16352, 16416])
+def test_rows_where_granules_a_thread_change(K):
+    test_rows_alone_and_among_many(K)
+
+
 def back_bounds(dy, h, rstd, w, dh):
     """dx and dweight in 64 bits, and their error bounds."""
     n = h.double() * rstd.double().unsqueeze(-1)
