@@ -24,15 +24,15 @@ namespace mxq {
 namespace {
 
 // Rows a lane (mx_tile.cuh), four CTAs an SM each.  8192 x 14336, both ways out,
-// measured on GB300 before AHEAD: forward 153 us with 4 rows (32 warps an SM, 64 registers)
+// measured on GB300 before the prefetch below: forward 153 us with 4 rows (32 warps an SM, 64 registers)
 // and 165 us with 8 (three CTAs: 128 registers spill); backward, which issues twice the
 // instructions a value, 180 us with 4 and 170 us with 8 (169 us since).
 constexpr int SAVE_LR = 4, BACK_LR = 8;
-// Forward, a CTA has the operands of the tile half a wave on brought into L2 (two tiles an
+constexpr int CTAS = 4;      // an SM
+// Forward, a CTA has the operands of the tile half a wave on brought into L2 (CTAS / 2 an
 // SM; with a whole wave 152 us, with two 192, without 156): its successor waits for L2
 // instead of memory.  The backward pass waits for instructions: 168.4 us with, 168.7
 // without.
-constexpr int AHEAD = 304;
 constexpr int BF16_PITCH = MX_TILE_K * 2;
 constexpr int BF16_TILE = TILE_ROWS * BF16_PITCH;
 constexpr int CODE_TILE = TILE_ROWS * MX_TILE_K;
@@ -91,7 +91,7 @@ struct GatedSaveShared {
 };
 
 template <int MODE, bool GELU>
-__global__ void __launch_bounds__(Tile<SAVE_LR>::THREADS, 4)
+__global__ void __launch_bounds__(Tile<SAVE_LR>::THREADS, CTAS)
 mx_gated_save_kernel(const __grid_constant__ CUtensorMap tmap_x,
                      const __grid_constant__ CUtensorMap tmap_qcol, const SavedArgs a) {
   using L = GatedSaveShared;
@@ -109,7 +109,7 @@ mx_gated_save_kernel(const __grid_constant__ CUtensorMap tmap_x,
     mbar_arrive_expect_tx(bar, 2 * BF16_TILE);
     tma_load_2d(sbase, &tmap_x, col0, row0, bar);
     tma_load_2d(sbase + L::UP, &tmap_x, a.N + col0, row0, bar);
-    const int tile = static_cast<int>(blockIdx.x) + AHEAD;
+    const int tile = static_cast<int>(blockIdx.x) + a.ahead;
     if (tile < static_cast<int>(gridDim.x)) {
       const int x = tile % a.tiles_k * MX_TILE_K, y = tile / a.tiles_k * TILE_ROWS;
       tma_prefetch_2d(&tmap_x, x, y);
@@ -249,7 +249,7 @@ __device__ __forceinline__ uint32_t e8m0_bits(uint32_t code) {
 }
 
 template <int MODE, bool GELU>
-__global__ void __launch_bounds__(Tile<BACK_LR>::THREADS, 4)
+__global__ void __launch_bounds__(Tile<BACK_LR>::THREADS, CTAS)
 mx_dgated_saved_kernel(const __grid_constant__ CUtensorMap tmap_grad,
                        const __grid_constant__ CUtensorMap tmap_saved,
                        const __grid_constant__ CUtensorMap tmap_qcol,
@@ -387,6 +387,7 @@ cudaError_t dgated_saved(const SavedMaps& maps, const SavedArgs& a, cudaStream_t
 }  // namespace
 
 int saved_tile_rows() { return TILE_ROWS; }
+int saved_prefetch(int num_sms) { return num_sms * CTAS / 2; }
 
 cudaError_t launch_gated_save(const SavedMaps& maps, const SavedArgs& a, int mode, bool gelu,
                               cudaStream_t stream) {

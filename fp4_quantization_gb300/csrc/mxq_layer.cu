@@ -186,6 +186,7 @@ mxq_status mx_quantize_gated_save(const void* x, int64_t M, int64_t N, int64_t l
   a.M = static_cast<int>(M);
   a.N = static_cast<int>(N);
   a.tiles_k = (a.N + mxq::MX_TILE_K - 1) / mxq::MX_TILE_K;
+  a.ahead = mxq::saved_prefetch(sms);
   a.scale_ceil = (flags & MXQ_SCALE_RCEIL) != 0;
   a.scale_tiled = (flags & MXQ_SCALE_SWIZZLED) != 0;
   a.q_row = q_row;

@@ -67,6 +67,7 @@ cudaError_t launch_norm_back(const NormBackArgs& a, int parts, float* dweight, c
 struct SavedArgs {
   int M, N;
   int tiles_k;                // 128-column tiles over N
+  int ahead;                  // forward: tiles from one to that which it prefetches
   int scale_ceil, scale_tiled;
   uint8_t* q_row;
   uint8_t* s_row;
@@ -85,8 +86,9 @@ struct SavedMaps {
   CUtensorMap q_col2;         // backward: those of d up
 };
 
-// Rows of a tile (64 or 128).
+// Rows of a tile, and how many tiles ahead the forward pass prefetches.
 int saved_tile_rows();
+int saved_prefetch(int num_sms);
 cudaError_t launch_gated_save(const SavedMaps& maps, const SavedArgs& a, int mode, bool gelu,
                               cudaStream_t stream);
 cudaError_t launch_dgated_saved(const SavedMaps& maps, const SavedArgs& a, int mode, bool gelu,

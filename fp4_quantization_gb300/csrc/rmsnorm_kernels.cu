@@ -279,16 +279,17 @@ rmsnorm_rows_kernel(const NormArgs a) {
 constexpr int LR = 8;
 constexpr int TILE_THREADS = Tile<LR>::THREADS;
 constexpr int TILE_SCALES_BYTES = Tile<LR>::SCALES_BYTES;
-// A CTA has the tile half a wave on brought into L2: 192.4 us with the row pass instead of
-// 197.4 (a quarter of a wave 193.6, a whole one 193.2).
-constexpr int AHEAD = 456;
+constexpr int COL_CTAS = 6;      // an SM
+// A CTA has the tile half a wave on (COL_CTAS / 2 an SM) brought into L2: 192.4 us with the
+// row pass instead of 197.4 (a quarter of a wave 193.6, a whole one 193.2).
 constexpr int COL_TILE_BYTES = TILE_ROWS * MX_TILE_K * 2;
 constexpr int COL_SHARED = COL_TILE_BYTES + TILE_SCALES_BYTES;
 
-__global__ void __launch_bounds__(TILE_THREADS, 6)
+__global__ void __launch_bounds__(TILE_THREADS, COL_CTAS)
 rmsnorm_cols_kernel(const __grid_constant__ CUtensorMap tmap_h,
                     const __grid_constant__ CUtensorMap tmap_qcol, const NormArgs a,
-                    uint8_t* s_col, int tiles_k, uint32_t* dev_err, uint64_t timeout_ns) {
+                    uint8_t* s_col, int tiles_k, int ahead, uint32_t* dev_err,
+                    uint64_t timeout_ns) {
   __shared__ __align__(1024) uint8_t smem[COL_SHARED];
   __shared__ __align__(8) uint64_t full;
   const uint32_t sbase = smem_addr(smem), bar = smem_addr(&full);
@@ -305,8 +306,8 @@ rmsnorm_cols_kernel(const __grid_constant__ CUtensorMap tmap_h,
   if (tid == 0) {
     mbar_arrive_expect_tx(bar, COL_TILE_BYTES);
     tma_load_2d(sbase, &tmap_h, col0, row0, bar);
-    if (tile >= AHEAD)
-      tma_prefetch_2d(&tmap_h, (tile - AHEAD) % tiles_k * MX_TILE_K, (tile - AHEAD) / tiles_k * TILE_ROWS);
+    if (tile >= ahead)
+      tma_prefetch_2d(&tmap_h, (tile - ahead) % tiles_k * MX_TILE_K, (tile - ahead) / tiles_k * TILE_ROWS);
   }
   float2 w[4];
   if (col0 + 8 * c < a.K) load_weight(a.weight, a.weight_f32, col0 + 8 * c, w);
@@ -672,7 +673,8 @@ cudaError_t launch_norm_both(const CUtensorMap& h, const CUtensorMap& q_col, con
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rmsnorm_cols_kernel, h, q_col, a, s_col, tiles_k, dev_err, timeout_ns);
+  return cudaLaunchKernelEx(&cfg, rmsnorm_cols_kernel, h, q_col, a, s_col, tiles_k,
+                            num_sms * COL_CTAS / 2, dev_err, timeout_ns);
 }
 
 // As many CTAs as are resident at once, each of which takes as many rows as another.
