@@ -25,9 +25,9 @@ namespace cg = cooperative_groups;
 
 constexpr uint32_t FULL = 0xFFFFFFFFu;
 constexpr int ROUTE_WARPS = 4;
-// CTAs of 128 threads an SM: 64 registers a thread, of which a few spill from six experts a
-// lane on (16384 tokens, 8 of 512 with a bias: 25.9 us, with 80 registers 26.4; 8 of 384
-// 17.4 and 18.4).
+// CTAs of 128 threads an SM: 64 registers a thread, of which a few spill from twelve
+// experts a lane on (16384 tokens, 8 of 512 with a bias: 25.1 us, with 80 registers 26.4; 8
+// of 384 17.4 and 18.4).
 constexpr int ROUTE_CTAS = 8;
 
 __device__ __forceinline__ float infinity() { return __int_as_float(0x7F800000); }

@@ -527,8 +527,10 @@ MXQ_API mxq_status mx_quantize_gated_save(const void* x, int64_t M, int64_t N, i
  *
  * Operation: as mx_quantize_dgated, with x[m][k] = E4M3(x_q[m][k]) *
  * 2^(x_s[m][k / 32] - 127) in fp32 (exact; a scale code of 255 is NaN).  The
- * activation and its slope come from one sigmoid: their last fp32 bits, and so a
- * code at a rounding's border, may differ from mx_quantize_dgated's.
+ * activation and its slope come from one sigmoid s, the slope as s plus a multiple of
+ * x - x s, which cancels where s is near 1: the slope (of at most 1.13) is off by up to
+ * 2^-17, where mx_quantize_dgated's is by a few fp32 ulps.  A code at a rounding's
+ * border may so differ from mx_quantize_dgated's.
  * x_q and x_s are those of mx_quantize_gated_save, or of mx_quantize_rowcol with
  * MXQ_ROWWISE and row-major scales.  MXQ_SCALE_SWIZZLED needs N % 128 == 0.
  */
@@ -546,8 +548,9 @@ MXQ_API mxq_status mx_quantize_dgated_saved(const void* grad, int64_t ldg, const
  * `groups` groups of E / groups consecutive experts the `kept` with the largest
  * sum of their two largest keys (the one key of groups of one expert; the largest
  * key with MXQ_ROUTE_GROUP_MAX) are kept; the key of an expert that is not
- * available is -inf, so that groups with fewer than two available come last.  The k experts with the largest keys of
- * those (without a bias: with the largest logits) are chosen, in that order; ties
+ * available is -inf, so that groups with fewer than two available come last.  The
+ * k experts with the largest keys of those (without a bias: with the largest
+ * logits) are chosen, in that order; ties
  * go to the lower expert or group.  weights[t][i] = scale * s of the i-th, divided
  * by the sum of the k chosen scores with MXQ_ROUTE_RENORM.
  * The choice is that of exact scores: keys are computed in fp32, and again in 64
