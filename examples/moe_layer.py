@@ -15,7 +15,8 @@ df_j = p_j dy and dp_j = dy . f_j.  Without weights every p_j is one.  Rows are 
 by expert, each expert's padded with zero rows to a multiple of 32, so that no block of
 32 rows belongs to two experts.  block_step and block_decode put the residual's
 addition, the norm and the router around it.  Decoding multiplies the
-few rows of a step with the experts' 4-bit weights where they lie.
+few rows of a step with the experts' 4-bit weights where they lie.  dense_step is
+the block without experts, whose norm hands its codes to the products.
 """
 import os
 import sys
@@ -109,6 +110,31 @@ def block_step(x, residual, gamma, router, k, w1, w2, dout):
     return h + f, back["dx"], back["dweight"], dlogits.t() @ y.float(), dw1, dw2
 
 
+def dense_step(x, residual, gamma, w1, w2, dout):
+    """A training step of a dense block, out = h + f(y) with h = x + residual and y its
+    RMSNorm times gamma [H].  The norm's own codes are what the products take: rows
+    forward, columns for dW1.  x, residual, dout [T, H] bf16, T a multiple of 32, w1
+    [1, 2F, H] and w2 [1, H, F] as MXWeights: out, and the gradients of x (and of the
+    residual alike), gamma and both weights."""
+    offsets = torch.arange(2, dtype=torch.int32, device=x.device) * len(x)
+
+    def rows_product(q, w, w_s):
+        return mxq.mx_grouped_gemm(q["q_row"], q["s_row"], w, w_s, offsets)
+
+    def gradient(g, x):
+        return mxq.mx_grouped_wgrad(g["q_col"], g["s_col"], x["q_col"], x["s_col"], offsets)
+
+    n = mxq.mx_rmsnorm(x, gamma, residual=residual)
+    hq = mxq.mx_quantize_gated_save(rows_product(n, w1.q, w1.s))
+    f = rows_product(hq, w2.q, w2.s)
+
+    gq = mxq.mx_quantize_rowcol(dout)
+    dgq = mxq.mx_quantize_dgated_saved(rows_product(gq, w2.q_t, w2.s_t), hq["x_q"], hq["x_s"])
+    dy = rows_product(dgq, w1.q_t, w1.s_t)
+    back = mxq.mx_rmsnorm_backward(dy, n["h"], n["rstd"], gamma, dh=dout)
+    return n["h"] + f, back["dx"], back["dweight"], gradient(dgq, n), gradient(gq, hq)
+
+
 class NVWeights:
     """An expert stack [E, N, K] in NVFP4 along its rows."""
 
@@ -159,6 +185,9 @@ def main():
     out = block_step(x, draw(T, H), gamma, router, k, MXWeights(w1), MXWeights(w2), dy)
     print("block:", *(f"{n} {tuple(t.shape)} norm {t.float().norm():.4g}"
                       for n, t in zip(("out", "dx", "dgamma", "drouter", "dw1", "dw2"), out)))
+    out = dense_step(x, draw(T, H), gamma, MXWeights(w1[:1]), MXWeights(w2[:1]), dy)
+    print("dense:", *(f"{n} {tuple(t.shape)} norm {t.float().norm():.4g}"
+                      for n, t in zip(("out", "dx", "dgamma", "dw1", "dw2"), out)))
 
 
 if __name__ == "__main__":
