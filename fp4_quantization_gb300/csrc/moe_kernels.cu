@@ -755,7 +755,8 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) moe_route_back_kernel(const 
 // distributed shared memory, over the CTAs.  Pairs are then put in order in shared
 // memory, so that `source` leaves in runs instead of 4 bytes a line.  131072 pairs over
 // 256 experts 16 us (eight CTAs that read the pairs twice and scattered `source` 37 us),
-// 32 pairs 4.8 us (device); what is left is shared memory's bank conflicts in 16 SMs,
+// 32 pairs 4.8 us (device); past 262144 pairs, which registers do not hold, 524288 65 us and
+// 2097152 243 us; what is left is shared memory's bank conflicts in 16 SMs,
 // and a grid over all SMs would need a second launch and a workspace.
 constexpr int SORT_CLUSTER = 16;
 constexpr int SORT_ITEMS = 16;            // pairs a lane that are kept in registers

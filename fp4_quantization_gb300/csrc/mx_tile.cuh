@@ -64,8 +64,8 @@ struct TileOut {
 // t, a row each at least: parts of 32-byte sectors that neighbouring tiles complete, kept
 // in L2 until they are whole.  `words`: all of them are aligned and four; else `n` exist,
 // and neighbouring lanes have a row's bytes, so that they are one write of L2 as well
-// (8192 x 14304: with a row's bytes by one lane 190 us forward and 193 backward, 160 and
-// 177 now).
+// (8192 x 14304: with a row's bytes by one lane 190 us forward and 193 backward, so 160
+// and 177).
 template <int THREADS>
 __device__ __forceinline__ void store_row_scales(uint32_t src, int lines, uint8_t* p,
                                                  int64_t pitch, bool words, int n, int t) {

@@ -550,12 +550,12 @@ MXQ_API mxq_status mx_quantize_dgated_saved(const void* grad, int64_t ldg, const
  * key with MXQ_ROUTE_GROUP_MAX) are kept; the key of an expert that is not
  * available is -inf, so that groups with fewer than two available come last.  The
  * k experts with the largest keys of those (without a bias: with the largest
- * logits) are chosen, in that order; ties
- * go to the lower expert or group.  weights[t][i] = scale * s of the i-th, divided
- * by the sum of the k chosen scores with MXQ_ROUTE_RENORM.
- * The choice is that of exact scores: keys are computed in fp32, and again in 64
- * bits where fp32 does not decide.  Weights are fp32; renormalised ones are ratios
- * that hold however small the scores are.
+ * logits) are chosen, in that order; ties go to the lower expert or group.
+ * weights[t][i] = scale * s of the i-th, divided by the sum of the k chosen scores
+ * with MXQ_ROUTE_RENORM.
+ * The choice is that of exact scores, as far as 64 bits tell them apart: keys are
+ * computed in fp32, and again in 64 bits where fp32 does not decide.  Weights are
+ * fp32; renormalised ones are ratios that hold however small the scores are.
  *
  *   logits  [T][ldl] bf16, or fp32 with MXQ_IN_F32, aligned to the element; any
  *           stride ldl >= E.  A logit of -inf (not the type's lowest value) is an
