@@ -591,8 +591,8 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, ROUTE_CTAS) moe_route_kernel
         const float xl = __shfl_sync(FULL, x, a.slots - 1), bl = __shfl_sync(FULL, b, a.slots - 1);
 #pragma unroll 1
         for (int e = lane; e < a.experts; e += 32) {
-          const float k = sk[e];
-          if (k > none && last - k <= 2.0f * err + 1.2e-7f * (fabsf(last) + fabsf(k)))
+          const float k = sk[e];          // (larger ones are chosen, or of groups not kept)
+          if (k > none && k <= last && last - k <= 2.0f * err + 1.2e-7f * (fabsf(last) + fabsf(k)))
             differ = differ || sl[e] != xl || a.bias[e] != bl;
         }
       }
