@@ -38,6 +38,8 @@
  *    (codes, scales, dbias, the global scale) is undefined.
  *  * Alignment: `x`, every output and the workspace 16-byte aligned, `ldx`
  *    a multiple of 8.  Violations return MXQ_EALIGN.
+ *  * A workspace serves one call at a time: calls that may overlap on the GPU
+ *    (on two streams, or in two graphs that are replayed) take one each.
  *  * The device must be compute capability 10.3 (GB300): else MXQ_EARCH.
  *  * NaN or infinite inputs are outside the contract.
  */
